@@ -79,10 +79,13 @@ typedef enum {
     SG_KERNEL_PREFETCH = 7,     /* side-stream weight prefetch                     */
     SG_KERNEL_ROUTER_TOPK = 8,  /* router top-k expert selection                   */
     SG_KERNEL_MXFP4 = 9,        /* projection with block-scaled 4-bit weights      */
-    SG_KERNEL_FP8 = 10          /* projection with block-scaled 8-bit weights      */
+    SG_KERNEL_FP8 = 10,         /* projection with block-scaled 8-bit weights      */
+    SG_KERNEL_INT8 = 11,        /* product of int8 codes (main launch)             */
+    SG_KERNEL_RMSNORM = 12,     /* root-mean-square norm (+ residual, int8 codes)  */
+    SG_KERNEL_QUANT_INT8 = 13   /* per-row int8 codes (optionally of a gated product) */
 } sg_kernel;
 
-#define SG_NUM_COUNTERS 11
+#define SG_NUM_COUNTERS 14
 #define SG_MAX_M 64
 
 /* Launch decision for one projection shape.  Produced by skinny_gemm_plan
@@ -292,6 +295,103 @@ sg_status skinny_gemm_fp8(int32_t M, int32_t N, int32_t K, const sg_bf16* x,
  * one-launch kernels, one split, or sizes the call rejects). */
 size_t skinny_gemm_fp8_workspace(int32_t M, int32_t N, int32_t K);
 size_t skinny_gemm_mxfp4_workspace(int32_t M, int32_t N, int32_t K);
+
+/* ---- 8-bit integer operators: codes and scales for each token and channel ----
+ *
+ * Integer projections take activations that were quantised a row (token) at a
+ * time and weights quantised a row (output channel) at a time.  The three
+ * calls below make the codes and use them; skinny_mlp_int8_step runs a whole
+ * gated MLP block of them.  They serve batches of any size up to SG_INT8_MAX_M
+ * rows: a caller that holds int8 weights has no other path for its prompts.
+ *
+ * Codes of a row v[0..K): amax = max_k |v[k]|, code[k] = round-half-even(v[k]
+ * * (127 / amax)) in fp32, scale = amax / 127 (so v is about code * scale;
+ * codes lie in [-127, 127]).  A row of zeros has codes 0 and scale 0.  A row
+ * that holds a NaN or an infinity (or whose fp32 intermediates overflow) has
+ * codes 0 and scale NaN, so everything computed from it is NaN.
+ * Rows never depend on each other, and repeated calls give identical bits. */
+#define SG_INT8_MAX_M (1 << 20)
+#define SG_INT8_MAX_K 131056 /* 2^14 * K < 2^31: every sum of products is exact */
+#define SG_ROW_MAX_K 65536   /* a row is held in the registers of one workgroup */
+
+/* Root-mean-square norm with the residual addition, and int8 output:
+ *   s = x + r (fp32; r NULL: s = x);  h = bf16(s);
+ *   y = s * g / sqrt(mean_k s^2 + eps)   (from s before its rounding to h).
+ * x, r [M, K], g [K] bf16.  Outputs, each NULL to skip, at least one of
+ * y_bf16 and codes: h [M, K] bf16, y_bf16 [M, K] bf16 (for the bf16, FP8 and
+ * MXFP4 projections), codes [M, K] int8 with scales [M] fp32 (for
+ * skinny_gemm_int8; given together).  The codes are those of s * g, from which
+ * the row's common factor cancels.  h and y_bf16 may each be the same buffer
+ * as x or r (not as one another); any other overlap is undefined.
+ * Limits: 0 <= M <= SG_INT8_MAX_M, 1 <= K <= SG_ROW_MAX_K, eps positive and
+ * finite (else SG_ERR_SHAPE); K % 8 == 0, pointers 16-byte aligned (scales
+ * 4-byte) (else SG_ERR_ALIGN). */
+sg_status skinny_rmsnorm(int32_t M, int32_t K, const sg_bf16* x, const sg_bf16* r,
+                         const sg_bf16* g, float eps, sg_bf16* h, sg_bf16* y_bf16, int8_t* codes,
+                         float* scales, void* stream);
+
+/* Codes [M, K] and scales [M] of the rows of x, given as x_bf16 or x_f32
+ * (exactly one non-NULL).  gated == 0: x [M, K], v = x -- activations in front
+ * of an integer projection, or (M = N) the channels of a weight matrix.
+ * gated == 1: x [M, 2K] holds gate rows then up rows, v = silu(gate) * up =
+ * gate / (1 + exp(-gate)) * up in fp32, not rounded before the codes.
+ * Limits: 0 <= M <= SG_INT8_MAX_M, 1 <= K <= SG_ROW_MAX_K, gated 0 or 1 (else
+ * SG_ERR_SHAPE); K % 8 == 0, pointers 16-byte aligned (scales 4-byte) (else
+ * SG_ERR_ALIGN).  Outputs must not overlap x. */
+sg_status skinny_quant_int8(int32_t M, int32_t K, const sg_bf16* x_bf16, const float* x_f32,
+                            int32_t gated, int8_t* codes, float* scales, void* stream);
+
+/* y[m,n] = (sum_k x_codes[m,k] * W_codes[n,k]) * W_scales[n] * x_scales[m].
+ * x_codes [M, K], W_codes [N, K] int8 (all of -128..127), x_scales [M],
+ * W_scales [N] fp32.  The sum is exact (int32); its conversion to fp32 and
+ * the two products round once each, so the bits do not depend on how the work
+ * is split.  y_f32 and/or y_bf16 [M, N] (at least one); r (nullable) bf16
+ * [M, N] gives the fused residual bf16_RNE(fp32(r) + y), y_bf16 may equal r.
+ * A NaN or infinite scale follows fp32's rules (0 * infinity is NaN).
+ * workspace: skinny_gemm_int8_workspace bytes (16-byte aligned; NULL when
+ * that is 0), for the int32 partial sums of a K split between workgroups.
+ * Limits: 0 <= M <= SG_INT8_MAX_M, 0 <= N <= 1<<20, 0 <= K <= SG_INT8_MAX_K
+ * (else SG_ERR_SHAPE); K % 16 == 0, codes, r, outputs and workspace 16-byte
+ * aligned, scales 4-byte (else SG_ERR_ALIGN). */
+sg_status skinny_gemm_int8(int32_t M, int32_t N, int32_t K, const int8_t* x_codes,
+                           const float* x_scales, const int8_t* W_codes, const float* W_scales,
+                           const sg_bf16* r, float* y_f32, sg_bf16* y_bf16, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Workspace bytes skinny_gemm_int8 needs (0 if none, or the sizes are rejected). */
+size_t skinny_gemm_int8_workspace(int32_t M, int32_t N, int32_t K);
+
+/* A gated MLP block with int8 weights:
+ *   h   = x (+ r);   q, sq = int8 codes of rmsnorm(h) * g       (skinny_rmsnorm)
+ *   u   = q W_gate_up^T, fp32                                   (skinny_gemm_int8)
+ *   p, sp = int8 codes of silu(u[:, :F]) * u[:, F:]             (skinny_quant_int8)
+ *   out = bf16(bf16(h) + p W_down^T)                            (skinny_gemm_int8)
+ * x, r [M, H] bf16 (r NULL: none), g [H] bf16; W_gate_up [2F, H] int8 (gate
+ * rows, then up rows) with scales [2F]; W_down [H, F] int8 with scales [H];
+ * out [M, H] bf16, which may be x's or r's buffer.  Nothing else may overlap.
+ * Limits: 0 <= M <= SG_INT8_MAX_M, 16 <= H <= SG_ROW_MAX_K, 16 <= F <=
+ * SG_ROW_MAX_K, eps positive and finite (else SG_ERR_SHAPE); H % 16 == 0,
+ * F % 16 == 0, pointers 16-byte aligned (scales 4-byte) (else SG_ERR_ALIGN).
+ * Workspace: skinny_mlp_int8_step_workspace bytes, 16-byte aligned, holds the
+ * codes, scales and u between the launches. */
+typedef struct {
+    const sg_bf16* x;
+    const sg_bf16* r;
+    const sg_bf16* g;
+    const int8_t* W_gate_up;
+    const float* gate_up_scales;
+    const int8_t* W_down;
+    const float* down_scales;
+    sg_bf16* out;
+    int32_t M, H, F;
+    float eps;
+} sg_mlp_int8_step;
+
+/* Workspace bytes skinny_mlp_int8_step needs (0 if the sizes are rejected). */
+size_t skinny_mlp_int8_step_workspace(int32_t M, int32_t H, int32_t F);
+
+sg_status skinny_mlp_int8_step(const sg_mlp_int8_step* step, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* One MoE decode step of a layer on one GPU, with the shared expert on its
  * own stream ([P] Method details §3; [F] Partie 1 §3: the shared expert runs

@@ -20,7 +20,8 @@ from ._lib import (KERNEL_NAMES, SG_KERNEL_GEMV, SG_KERNEL_GROUPED, SG_KERNEL_MO
                    SG_KERNEL_FP8, SG_KERNEL_MXFP4, SG_KERNEL_NONE, SG_KERNEL_PREFETCH, SG_KERNEL_REDUCE,
                    SG_KERNEL_ROUTER_TOPK,
                    SG_KERNEL_SPLITK_MFMA, SG_KERNEL_SPLITK_VALU, SG_NOALLOC_MAX_WORKSPACE,
-                   SG_NUM_COUNTERS, SgMoeStep,
+                   SG_KERNEL_INT8, SG_KERNEL_QUANT_INT8, SG_KERNEL_RMSNORM,
+                   SG_NUM_COUNTERS, SgMlpInt8Step, SgMoeStep,
                    SgPlan, SkinnyGemmError)
 
 __all__ = [
@@ -30,6 +31,9 @@ __all__ = [
     "skinny_gemm_router_topk", "router_topk", "skinny_moe_step_workspace", "skinny_moe_step",
     "concat_router_shared", "MOE_STEP_MODES", "skinny_gemm_mxfp4", "SG_KERNEL_MXFP4",
     "skinny_gemm_fp8", "SG_KERNEL_FP8", "skinny_gemm_fp8_workspace", "skinny_gemm_mxfp4_workspace",
+    "skinny_rmsnorm", "skinny_quant_int8", "skinny_gemm_int8", "skinny_gemm_int8_workspace",
+    "skinny_mlp_int8_step", "skinny_mlp_int8_step_workspace",
+    "SG_KERNEL_INT8", "SG_KERNEL_RMSNORM", "SG_KERNEL_QUANT_INT8",
     "skinny_gemm_status_str", "skinny_gemm_get_counters", "skinny_gemm_reset_counters",
     "SgPlan", "SkinnyGemmError", "KERNEL_NAMES", "SG_KERNEL_NONE", "SG_KERNEL_GEMV",
     "SG_KERNEL_SPLITK_VALU", "SG_KERNEL_SPLITK_MFMA", "SG_KERNEL_REDUCE", "SG_KERNEL_MOE_TABLE",
@@ -335,6 +339,165 @@ def skinny_gemm_fp8(x: torch.Tensor, W_codes: torch.Tensor, W_scales: torch.Tens
         _stream(stream))
     _lib.check(st)
     return y_f32, y_bf16
+
+
+# ---- 8-bit integer operators: codes with one scale per row (token or channel) ----
+
+
+def _arg(t, dtype, shape, name, dev):
+    """Device pointer of a contiguous tensor of exactly this type, shape and device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_cuda and t.is_contiguous()):
+        return t.data_ptr() or None
+    _ptr(t, dtype, name, dev)
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _opt(t, dtype, shape, name, dev):
+    return None if t is None else _arg(t, dtype, shape, name, dev)
+
+
+def _rows(x, name, dtypes):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(x).__name__}")
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(x.shape)}")
+    return x.shape[0], x.shape[1], x.device
+
+
+def _new(shape, dtype, dev, stream):
+    """A tensor the work on `stream` may use at once: taken from that stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _ws_arg(workspace, nbytes, dev, stream):
+    """(tensor, pointer, bytes) of the given workspace, or of a new one when none is given."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = _new((nbytes,), torch.uint8, dev, stream)
+    return workspace, _ptr(workspace, torch.uint8, "workspace", dev), workspace.numel()
+
+
+def _run_on(dev, stream, fn, *args):
+    """fn(*args, stream handle) with dev current; the default stream is dev's current one."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None
+                else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    if st:
+        _lib.check(st)
+
+
+def skinny_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, r=None, h=None, y_bf16=None,
+                   codes=None, scales=None, stream=None):
+    """Root-mean-square norm with the residual addition and int8 output: s = x (+ r), h = bf16(s),
+    y = s * g / sqrt(mean(s^2) + eps).  x, r [M, K], g [K] bf16.  Writes what is given of h and
+    y_bf16 (bf16 [M, K], each may be x or r itself) and codes int8 [M, K] with scales float32 [M]
+    (y is about codes * scales[:, None]); allocates codes and scales when neither y_bf16 nor codes
+    is given, and scales when only codes is.  Returns (h, y_bf16, codes, scales)."""
+    M, K, dev = _rows(x, "x", (torch.bfloat16,))
+    if codes is None and (y_bf16 is None or scales is not None):
+        codes = _new((M, K), torch.int8, dev, stream)
+    if codes is not None and scales is None:
+        scales = _new((M,), torch.float32, dev, stream)
+    bf16, mk = torch.bfloat16, (M, K)
+    _run_on(dev, stream, _c().skinny_rmsnorm, M, K, _arg(x, bf16, mk, "x", dev),
+            _opt(r, bf16, mk, "r", dev), _arg(g, bf16, (K,), "g", dev), eps,
+            _opt(h, bf16, mk, "h", dev), _opt(y_bf16, bf16, mk, "y_bf16", dev),
+            _opt(codes, torch.int8, mk, "codes", dev),
+            _opt(scales, torch.float32, (M,), "scales", dev))
+    return h, y_bf16, codes, scales
+
+
+def skinny_quant_int8(x: torch.Tensor, gated: bool = False, codes=None, scales=None, stream=None):
+    """Codes int8 [M, K] and scales float32 [M] of rows of x (bf16 or float32): of x [M, K]
+    itself, or with gated of silu(x[:, :K]) * x[:, K:] for x [M, 2K].  Rows are tokens in front
+    of an integer projection, or the channels of a weight matrix.  Returns (codes, scales)."""
+    M, K, dev = _rows(x, "x", (torch.bfloat16, torch.float32))
+    width = K
+    if gated:
+        if K % 2:
+            raise ValueError(f"x: gated rows hold gate and up halves, got {K} columns")
+        K //= 2
+    if codes is None:
+        codes = _new((M, K), torch.int8, dev, stream)
+    if scales is None:
+        scales = _new((M,), torch.float32, dev, stream)
+    px = _arg(x, x.dtype, (M, width), "x", dev)
+    f32 = x.dtype is torch.float32
+    _run_on(dev, stream, _c().skinny_quant_int8, M, K, None if f32 else px, px if f32 else None,
+            1 if gated else 0, _arg(codes, torch.int8, (M, K), "codes", dev),
+            _arg(scales, torch.float32, (M,), "scales", dev))
+    return codes, scales
+
+
+def skinny_gemm_int8_workspace(M: int, N: int, K: int) -> int:
+    """Workspace bytes skinny_gemm_int8 needs for an M x N x K product (0 when none)."""
+    return int(_c().skinny_gemm_int8_workspace(M, N, K))
+
+
+def skinny_gemm_int8(x_codes: torch.Tensor, x_scales: torch.Tensor, W_codes: torch.Tensor,
+                     W_scales: torch.Tensor, y_f32=None, y_bf16=None, r=None, workspace=None,
+                     stream=None):
+    """y[m, n] = sum_k x_codes[m, k] W_codes[n, k] * W_scales[n] * x_scales[m] for int8 codes
+    x_codes [M, K], W_codes [N, K] and float32 scales [M], [N]; any M up to 2^20.  Writes y_f32
+    and/or y_bf16 [M, N]; with r (bf16 [M, N]) the fused residual y = r + product (y_bf16 may
+    be r).  Allocates y_f32 when no output is given, and the workspace when one is needed and
+    none is given; returns the outputs."""
+    M, K, dev = _rows(x_codes, "x_codes", (torch.int8,))
+    N = _rows(W_codes, "W_codes", (torch.int8,))[0]
+    mn = (M, N)
+    if y_f32 is None and y_bf16 is None:
+        y_f32 = _new(mn, torch.float32, dev, stream)
+    ws, ws_ptr, ws_bytes = _ws_arg(workspace, _c().skinny_gemm_int8_workspace(M, N, K), dev, stream)
+    f32, bf16 = torch.float32, torch.bfloat16
+    _run_on(dev, stream, _c().skinny_gemm_int8, M, N, K,
+            _arg(x_codes, torch.int8, (M, K), "x_codes", dev),
+            _arg(x_scales, f32, (M,), "x_scales", dev),
+            _arg(W_codes, torch.int8, (N, K), "W_codes", dev),
+            _arg(W_scales, f32, (N,), "W_scales", dev), _opt(r, bf16, mn, "r", dev),
+            _opt(y_f32, f32, mn, "y_f32", dev), _opt(y_bf16, bf16, mn, "y_bf16", dev),
+            ws_ptr, ws_bytes)
+    return y_f32, y_bf16
+
+
+def skinny_mlp_int8_step_workspace(M: int, H: int, F: int) -> int:
+    """Workspace bytes skinny_mlp_int8_step needs (0 if the sizes are rejected)."""
+    return int(_c().skinny_mlp_int8_step_workspace(M, H, F))
+
+
+def skinny_mlp_int8_step(x: torch.Tensor, g: torch.Tensor, eps: float, W_gate_up: torch.Tensor,
+                         gate_up_scales: torch.Tensor, W_down: torch.Tensor,
+                         down_scales: torch.Tensor, r=None, out=None, workspace=None, stream=None):
+    """A gated MLP block with int8 weights: h = x (+ r), out = h + down(swiglu(gate_up(norm(h)))),
+    the norm's output and the gated product quantised a token at a time.  x, r [M, H], g [H] bf16;
+    W_gate_up int8 [2F, H] (gate rows, then up rows), W_down int8 [H, F], float32 scales per row.
+    out bf16 [M, H] (may be x or r itself; allocated when not given).  Returns out."""
+    M, H, dev = _rows(x, "x", (torch.bfloat16,))
+    F = _rows(W_down, "W_down", (torch.int8,))[1]
+    if out is None:
+        out = _new((M, H), torch.bfloat16, dev, stream)
+    ws, ws_ptr, ws_bytes = _ws_arg(workspace, _c().skinny_mlp_int8_step_workspace(M, H, F), dev,
+                                   stream)
+    i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
+    step = SgMlpInt8Step(
+        _arg(x, bf16, (M, H), "x", dev), _opt(r, bf16, (M, H), "r", dev),
+        _arg(g, bf16, (H,), "g", dev), _arg(W_gate_up, i8, (2 * F, H), "W_gate_up", dev),
+        _arg(gate_up_scales, f32, (2 * F,), "gate_up_scales", dev),
+        _arg(W_down, i8, (H, F), "W_down", dev), _arg(down_scales, f32, (H,), "down_scales", dev),
+        _arg(out, bf16, (M, H), "out", dev), M, H, F, eps)
+    _run_on(dev, stream, _c().skinny_mlp_int8_step, ctypes.byref(step), ws_ptr, ws_bytes)
+    return out
 
 
 def concat_router_shared(W_router: torch.Tensor, W_shared: torch.Tensor):

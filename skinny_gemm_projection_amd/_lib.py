@@ -26,10 +26,13 @@ SG_KERNEL_PREFETCH = 7
 SG_KERNEL_ROUTER_TOPK = 8
 SG_KERNEL_MXFP4 = 9
 SG_KERNEL_FP8 = 10
-SG_NUM_COUNTERS = 11
+SG_KERNEL_INT8 = 11
+SG_KERNEL_RMSNORM = 12
+SG_KERNEL_QUANT_INT8 = 13
+SG_NUM_COUNTERS = 14
 KERNEL_NAMES = {0: "none", 1: "gemv", 2: "splitk_valu", 3: "splitk_mfma", 4: "reduce",
                 5: "moe_table", 6: "grouped", 7: "prefetch", 8: "router_topk", 9: "mxfp4",
-                10: "fp8"}
+                10: "fp8", 11: "int8", 12: "rmsnorm", 13: "quant_int8"}
 
 
 class SgPlan(ctypes.Structure):
@@ -59,6 +62,16 @@ class SgMoeStep(ctypes.Structure):
                 ("T", ctypes.c_int32), ("K", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("topk", ctypes.c_int32), ("N", ctypes.c_int32), ("N_shared", ctypes.c_int32),
                 ("flags", ctypes.c_int32)]
+
+
+class SgMlpInt8Step(ctypes.Structure):
+    """Mirror of sg_mlp_int8_step."""
+    _fields_ = [("x", ctypes.c_void_p), ("r", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("W_gate_up", ctypes.c_void_p), ("gate_up_scales", ctypes.c_void_p),
+                ("W_down", ctypes.c_void_p), ("down_scales", ctypes.c_void_p),
+                ("out", ctypes.c_void_p),
+                ("M", ctypes.c_int32), ("H", ctypes.c_int32), ("F", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 SG_MOE_STEP_FUSED_SHARED = 1
@@ -104,6 +117,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in ("skinny_gemm_fp8_workspace", "skinny_gemm_mxfp4_workspace"):
         getattr(lib, name).argtypes = [i32, i32, i32]
         getattr(lib, name).restype = sz
+    f32 = ctypes.c_float
+    lib.skinny_rmsnorm.argtypes = [i32, i32, p, p, p, f32, p, p, p, p, p]
+    lib.skinny_quant_int8.argtypes = [i32, i32, p, p, i32, p, p, p]
+    lib.skinny_gemm_int8.argtypes = [i32, i32, i32, p, p, p, p, p, p, p, p, sz, p]
+    for name in ("skinny_gemm_int8_workspace", "skinny_mlp_int8_step_workspace"):
+        getattr(lib, name).argtypes = [i32, i32, i32]
+        getattr(lib, name).restype = sz
+    lib.skinny_mlp_int8_step.argtypes = [ctypes.POINTER(SgMlpInt8Step), p, sz, p]
     lib.skinny_moe_step_workspace.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.skinny_moe_step_workspace.restype = sz
     lib.skinny_moe_step.argtypes = [ctypes.POINTER(SgMoeStep), p, sz, p, p, p, p]
@@ -116,7 +137,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in ("skinny_gemm_plan", "skinny_gemm_plan_force", "skinny_gemm",
                  "skinny_gemm_residual", "skinny_gemm_noalloc", "grouped_skinny_gemm", "skinny_gemm_prefetch",
                  "skinny_gemm_router_topk", "skinny_moe_step", "skinny_gemm_mxfp4",
-                 "skinny_gemm_fp8"):
+                 "skinny_gemm_fp8", "skinny_rmsnorm", "skinny_quant_int8", "skinny_gemm_int8",
+                 "skinny_mlp_int8_step"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

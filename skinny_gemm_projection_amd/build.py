@@ -24,7 +24,7 @@ ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "plan.cpp", "moe_step.cpp", "rowdot.hip", "splitk_mfma.hip", "reduce.hip", "moe.hip", "router.hip", "mxfp4.hip",
            "prefetch.hip", "fp8.hip", "noalloc.hip", "lowp_chunk.hip",
-           "probe.hip"]
+           "probe.hip", "int8_api.cpp", "int8.hip", "norm_quant.hip"]
 
 
 def hipcc() -> str:

@@ -48,6 +48,9 @@ const char* kernel_name(int k) {
         case SG_KERNEL_FP8: return "fp8";
         case SG_KERNEL_ROUTER_TOPK: return "router_topk";
         case SG_KERNEL_MXFP4: return "mxfp4";
+        case SG_KERNEL_INT8: return "int8";
+        case SG_KERNEL_RMSNORM: return "rmsnorm";
+        case SG_KERNEL_QUANT_INT8: return "quant_int8";
         default: return "?";
     }
 }
@@ -115,6 +118,9 @@ bool grouped_sizes_ok(int32_t T, int32_t E, int32_t topk, int32_t N, int32_t K) 
 }  // namespace
 
 namespace sg {
+
+void count_launch(int kernel) { count(kernel); }
+bool launch_log_enabled() { return log_enabled(); }
 
 sg_status router_topk_call(const float* scores, int64_t ld, int32_t T, int32_t E, int32_t k,
                            int32_t* topk_ids, float* topk_scores, void* stream) {

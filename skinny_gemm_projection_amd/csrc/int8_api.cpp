@@ -1,0 +1,185 @@
+// int8_api.cpp -- the C ABI of the 8-bit integer operators (declared in
+// include/skinny_gemm.h): argument checks, launches and launch counts, and the
+// gated MLP step composed of them.  As for every other entry point, what the
+// host can see is refused before anything is launched, and an accepted call
+// only enqueues kernels on the caller's stream.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+
+#include "launch.h"
+#include "plan_internal.h"
+#include "skinny_gemm.h"
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool eps_ok(float eps) { return eps > 0.0f && std::isfinite(eps); }
+
+bool gemm_sizes_ok(int32_t M, int32_t N, int32_t K) {
+    return M >= 0 && M <= SG_INT8_MAX_M && N >= 0 && N <= (1 << 20) && K >= 0 && K <= SG_INT8_MAX_K;
+}
+
+bool rows_ok(int32_t M, int32_t K) {
+    return M >= 0 && M <= SG_INT8_MAX_M && K >= 1 && K <= SG_ROW_MAX_K;
+}
+
+// Byte offsets of the MLP step's intermediates in its workspace.
+struct MlpLayout {
+    size_t q, sq, u, p, sp, gemm, gemm_bytes, total;
+};
+
+bool mlp_layout(int32_t M, int32_t H, int32_t F, MlpLayout* L) {
+    if (M < 0 || M > SG_INT8_MAX_M || H < 16 || H > SG_ROW_MAX_K || F < 16 || F > SG_ROW_MAX_K ||
+        H % 16 != 0 || F % 16 != 0)
+        return false;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    const size_t m = (size_t)M;
+    L->q = take(m * H);
+    L->sq = take(m * 4);
+    L->u = take(m * F * 8);
+    L->p = take(m * F);
+    L->sp = take(m * 4);
+    const size_t a = M > 0 ? sg::int8_workspace_bytes(M, 2 * F, H) : 0;
+    const size_t b = M > 0 ? sg::int8_workspace_bytes(M, H, F) : 0;
+    L->gemm_bytes = a > b ? a : b;
+    L->gemm = take(L->gemm_bytes);
+    L->total = at;
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+sg_status skinny_rmsnorm(int32_t M, int32_t K, const sg_bf16* x, const sg_bf16* r,
+                         const sg_bf16* g, float eps, sg_bf16* h, sg_bf16* y_bf16, int8_t* codes,
+                         float* scales, void* stream) {
+    if (!rows_ok(M, K) || !eps_ok(eps)) return SG_ERR_SHAPE;
+    if (K % 8 != 0) return SG_ERR_ALIGN;
+    if (M == 0) return SG_OK;
+    if (!x || !g || (!y_bf16 && !codes) || (codes != nullptr) != (scales != nullptr))
+        return SG_ERR_NULL;
+    if (!aligned16(x) || !aligned16(r) || !aligned16(g) || !aligned16(h) || !aligned16(y_bf16) ||
+        !aligned16(codes) || !aligned4(scales))
+        return SG_ERR_ALIGN;
+    (void)hipGetLastError();
+    if (sg::launch_rmsnorm(M, K, x, r, g, eps, h, y_bf16, codes, scales,
+                           static_cast<hipStream_t>(stream)) != hipSuccess)
+        return SG_ERR_HIP;
+    sg::count_launch(SG_KERNEL_RMSNORM);
+    if (sg::launch_log_enabled())
+        std::fprintf(stderr, "[skinny_gemm] rmsnorm M=%d K=%d%s%s%s\n", M, K,
+                     r ? " residual" : "", y_bf16 ? " bf16" : "", codes ? " int8" : "");
+    return SG_OK;
+}
+
+sg_status skinny_quant_int8(int32_t M, int32_t K, const sg_bf16* x_bf16, const float* x_f32,
+                            int32_t gated, int8_t* codes, float* scales, void* stream) {
+    if (!rows_ok(M, K) || (gated != 0 && gated != 1)) return SG_ERR_SHAPE;
+    if (K % 8 != 0) return SG_ERR_ALIGN;
+    if (M == 0) return SG_OK;
+    if ((x_bf16 != nullptr) == (x_f32 != nullptr) || !codes || !scales) return SG_ERR_NULL;
+    if (!aligned16(x_bf16) || !aligned16(x_f32) || !aligned16(codes) || !aligned4(scales))
+        return SG_ERR_ALIGN;
+    (void)hipGetLastError();
+    const void* x = x_f32 ? static_cast<const void*>(x_f32) : x_bf16;
+    if (sg::launch_quant_int8(M, K, x, x_f32 != nullptr, gated != 0, codes, scales,
+                              static_cast<hipStream_t>(stream)) != hipSuccess)
+        return SG_ERR_HIP;
+    sg::count_launch(SG_KERNEL_QUANT_INT8);
+    if (sg::launch_log_enabled())
+        std::fprintf(stderr, "[skinny_gemm] quant_int8 M=%d K=%d %s%s\n", M, K,
+                     x_f32 ? "fp32" : "bf16", gated ? " gated" : "");
+    return SG_OK;
+}
+
+size_t skinny_gemm_int8_workspace(int32_t M, int32_t N, int32_t K) {
+    if (!gemm_sizes_ok(M, N, K) || K % 16 != 0 || M == 0 || N == 0) return 0;
+    return sg::int8_workspace_bytes(M, N, K);
+}
+
+sg_status skinny_gemm_int8(int32_t M, int32_t N, int32_t K, const int8_t* x_codes,
+                           const float* x_scales, const int8_t* W_codes, const float* W_scales,
+                           const sg_bf16* r, float* y_f32, sg_bf16* y_bf16, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    if (!gemm_sizes_ok(M, N, K)) return SG_ERR_SHAPE;
+    if (K % 16 != 0) return SG_ERR_ALIGN;
+    if (M == 0 || N == 0) return SG_OK;
+    if ((!y_f32 && !y_bf16) || !x_scales || !W_scales) return SG_ERR_NULL;
+    if (K > 0 && (!x_codes || !W_codes)) return SG_ERR_NULL;
+    if (!aligned16(x_codes) || !aligned16(W_codes) || !aligned4(x_scales) || !aligned4(W_scales) ||
+        !aligned16(r) || !aligned16(y_f32) || !aligned16(y_bf16))
+        return SG_ERR_ALIGN;
+    const size_t need = sg::int8_workspace_bytes(M, N, K);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return SG_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return SG_ERR_ALIGN;
+    }
+    (void)hipGetLastError();
+    const sg::Int8Epilogue ep{x_scales, W_scales, y_f32, y_bf16, r};
+    if (sg::launch_gemm_int8(M, N, K, x_codes, W_codes, ep, workspace,
+                             static_cast<hipStream_t>(stream)) != hipSuccess)
+        return SG_ERR_HIP;
+    sg::count_launch(SG_KERNEL_INT8);
+    if (sg::launch_log_enabled())
+        std::fprintf(stderr, "[skinny_gemm] int8 M=%d N=%d K=%d%s\n", M, N, K,
+                     r ? " residual" : "");
+    return SG_OK;
+}
+
+size_t skinny_mlp_int8_step_workspace(int32_t M, int32_t H, int32_t F) {
+    MlpLayout L;
+    return mlp_layout(M, H, F, &L) ? L.total : 0;
+}
+
+sg_status skinny_mlp_int8_step(const sg_mlp_int8_step* a, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    if (!a) return SG_ERR_NULL;
+    MlpLayout L;
+    if (!mlp_layout(a->M, a->H, a->F, &L))
+        return a->H > 0 && a->F > 0 && (a->H % 16 != 0 || a->F % 16 != 0) ? SG_ERR_ALIGN
+                                                                          : SG_ERR_SHAPE;
+    if (!eps_ok(a->eps)) return SG_ERR_SHAPE;
+    if (a->M == 0) return SG_OK;
+    // every check of the calls below, made here before the first launch
+    if (!a->x || !a->g || !a->W_gate_up || !a->gate_up_scales || !a->W_down || !a->down_scales ||
+        !a->out)
+        return SG_ERR_NULL;
+    if (!aligned16(a->x) || !aligned16(a->r) || !aligned16(a->g) || !aligned16(a->W_gate_up) ||
+        !aligned16(a->W_down) || !aligned16(a->out) || !aligned4(a->gate_up_scales) ||
+        !aligned4(a->down_scales))
+        return SG_ERR_ALIGN;
+    if (!workspace || workspace_bytes < L.total) return SG_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SG_ERR_ALIGN;
+
+    char* base = static_cast<char*>(workspace);
+    int8_t* q = reinterpret_cast<int8_t*>(base + L.q);
+    float* sq = reinterpret_cast<float*>(base + L.sq);
+    float* u = reinterpret_cast<float*>(base + L.u);
+    int8_t* p = reinterpret_cast<int8_t*>(base + L.p);
+    float* sp = reinterpret_cast<float*>(base + L.sp);
+    void* gw = base + L.gemm;
+    sg_status st;
+    // out holds h between the norm and the down projection, which adds to it
+    if ((st = skinny_rmsnorm(a->M, a->H, a->x, a->r, a->g, a->eps, a->out, nullptr, q, sq,
+                             stream)) != SG_OK)
+        return st;
+    if ((st = skinny_gemm_int8(a->M, 2 * a->F, a->H, q, sq, a->W_gate_up, a->gate_up_scales,
+                               nullptr, u, nullptr, gw, L.gemm_bytes, stream)) != SG_OK)
+        return st;
+    if ((st = skinny_quant_int8(a->M, a->F, nullptr, u, 1, p, sp, stream)) != SG_OK) return st;
+    return skinny_gemm_int8(a->M, a->H, a->F, p, sp, a->W_down, a->down_scales, a->out, nullptr,
+                            a->out, gw, L.gemm_bytes, stream);
+}
+
+}  // extern "C"

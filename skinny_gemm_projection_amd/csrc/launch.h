@@ -171,6 +171,26 @@ bool lowp_chunk_plan(int M, int N, int K, LowpChunkPlan* p);
 hipError_t launch_lowp_chunk(int fmt, int M, int N, int K, const void* x, const void* Wq,
                              const void* Ws, const Epilogue& fin, void* ws, hipStream_t stream);
 
+// Row operators (norm_quant.hip).  K a multiple of 8, 8 <= K <= SG_ROW_MAX_K.
+hipError_t launch_rmsnorm(int M, int K, const uint16_t* x, const uint16_t* r, const uint16_t* g,
+                          float eps, uint16_t* h, uint16_t* y, int8_t* codes, float* scales,
+                          hipStream_t stream);
+// x as bf16 (f32 == false) or fp32; gated: rows of 2K values.
+hipError_t launch_quant_int8(int M, int K, const void* x, bool f32, bool gated, int8_t* codes,
+                             float* scales, hipStream_t stream);
+
+// Product of int8 codes (int8.hip): M, N >= 1, K a multiple of 16.
+struct Int8Epilogue {
+    const float* xs;      // [M] token scales
+    const float* ws;      // [N] channel scales
+    float* y_f32;         // nullable
+    uint16_t* y_bf16;     // nullable; may equal r
+    const uint16_t* r;    // residual [M, N] or nullptr
+};
+size_t int8_workspace_bytes(int M, int N, int K);
+hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t* wq,
+                            const Int8Epilogue& ep, void* ws, hipStream_t stream);
+
 // Router top-k: ids [T,k] (and their scores) from fp32 scores, row t at
 // scores + t*ld (ld >= E); E <= 4096, k <= 32 (checked by the caller).
 hipError_t launch_router_topk(const float* scores, int64_t ld, int T, int E, int k,

@@ -10,6 +10,11 @@ namespace sg {
 sg_status make_plan(int32_t M, int32_t N, int32_t K, int32_t kernel, int32_t split_k,
                     int32_t two_pass, int32_t tile_n, sg_plan* out);
 
+// One launch of `kernel` (an sg_kernel) for the launch counters, and whether
+// SKINNY_GEMM_LOG asks for a line per launch decision.
+void count_launch(int kernel);
+bool launch_log_enabled();
+
 // True when *p is exactly what the planner produces for its own fields.
 bool plan_matches(const sg_plan* p);
 
