@@ -346,9 +346,11 @@ def skinny_gemm_fp8(x: torch.Tensor, W_codes: torch.Tensor, W_scales: torch.Tens
 
 def _arg(t, dtype, shape, name, dev):
     """Device pointer of a contiguous tensor of exactly this type, shape and device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
-            and t.is_cuda and t.is_contiguous()):
-        return t.data_ptr() or None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor: _ptr says so
+        pass
     _ptr(t, dtype, name, dev)
     raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
@@ -358,13 +360,17 @@ def _opt(t, dtype, shape, name, dev):
 
 
 def _rows(x, name, dtypes):
+    """(rows, columns, device) of a 2-D device tensor of one of the types."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(x).__name__}")
     if x.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
-    if x.dim() != 2:
-        raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(x.shape)}")
-    return x.shape[0], x.shape[1], x.device
+    if not x.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(shape)}")
+    return shape[0], shape[1], x.device
 
 
 def _new(shape, dtype, dev, stream):
@@ -386,14 +392,19 @@ def _ws_arg(workspace, nbytes, dev, stream):
     return workspace, _ptr(workspace, torch.uint8, "workspace", dev), workspace.numel()
 
 
+# The raw handle of a device's current stream; torch.cuda.current_stream makes a Stream object
+# first, which costs more host time than the rest of a call's argument checks.
+_current_stream = torch._C._cuda_getCurrentRawStream if torch.version.hip else None
+
+
 def _run_on(dev, stream, fn, *args):
     """fn(*args, stream handle) with dev current; the default stream is dev's current one."""
+    handle = _current_stream(dev.index) if stream is None else _stream(stream)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None
-                else _stream(stream))
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
+            st = fn(*args, handle)
     if st:
         _lib.check(st)
 
@@ -454,20 +465,20 @@ def skinny_gemm_int8(x_codes: torch.Tensor, x_scales: torch.Tensor, W_codes: tor
     and/or y_bf16 [M, N]; with r (bf16 [M, N]) the fused residual y = r + product (y_bf16 may
     be r).  Allocates y_f32 when no output is given, and the workspace when one is needed and
     none is given; returns the outputs."""
-    M, K, dev = _rows(x_codes, "x_codes", (torch.int8,))
-    N = _rows(W_codes, "W_codes", (torch.int8,))[0]
+    i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
+    M, K, dev = _rows(x_codes, "x_codes", (i8,))
+    N = _rows(W_codes, "W_codes", (i8,))[0]
     mn = (M, N)
+    c = _c()
     if y_f32 is None and y_bf16 is None:
         y_f32 = _new(mn, torch.float32, dev, stream)
-    ws, ws_ptr, ws_bytes = _ws_arg(workspace, _c().skinny_gemm_int8_workspace(M, N, K), dev, stream)
-    f32, bf16 = torch.float32, torch.bfloat16
-    _run_on(dev, stream, _c().skinny_gemm_int8, M, N, K,
-            _arg(x_codes, torch.int8, (M, K), "x_codes", dev),
-            _arg(x_scales, f32, (M,), "x_scales", dev),
-            _arg(W_codes, torch.int8, (N, K), "W_codes", dev),
-            _arg(W_scales, f32, (N,), "W_scales", dev), _opt(r, bf16, mn, "r", dev),
-            _opt(y_f32, f32, mn, "y_f32", dev), _opt(y_bf16, bf16, mn, "y_bf16", dev),
-            ws_ptr, ws_bytes)
+    ws, ws_ptr, ws_bytes = _ws_arg(workspace, c.skinny_gemm_int8_workspace(M, N, K), dev, stream)
+    _run_on(dev, stream, c.skinny_gemm_int8, M, N, K, _arg(x_codes, i8, (M, K), "x_codes", dev),
+            _arg(x_scales, f32, (M,), "x_scales", dev), _arg(W_codes, i8, (N, K), "W_codes", dev),
+            _arg(W_scales, f32, (N,), "W_scales", dev),
+            None if r is None else _arg(r, bf16, mn, "r", dev),
+            None if y_f32 is None else _arg(y_f32, f32, mn, "y_f32", dev),
+            None if y_bf16 is None else _arg(y_bf16, bf16, mn, "y_bf16", dev), ws_ptr, ws_bytes)
     return y_f32, y_bf16
 
 

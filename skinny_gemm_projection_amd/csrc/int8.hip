@@ -4,10 +4,26 @@
 //   y[m,n] = float(sum_k xq[m,k] * wq[n,k]) * ws[n] * xs[m]  (+ r, in fp32)
 //
 // v_mfma_i32_16x16x64_i8 multiplies 16 rows of W by 16 rows of x over 64
-// codes: lane (row = lane & 15, grp = lane >> 4) supplies the 16 codes
-// k = 16*grp .. +16 of its row, one 16-byte load, and receives
-// y[m = lane & 15][n = 4*grp .. +4], four neighbours of one row of y.  The
-// int32 sums are exact, so no split of K changes a bit.
+// codes: lane (row = lane & 15, grp = lane >> 4) supplies 16 codes of its row,
+// the same ones for W and x, and receives y[m = lane & 15][n = 4*grp .. +4],
+// four neighbours of one row of y.  The int32 sums are exact, so no split of K
+// changes a bit.
+//
+// Two kernels share the batch range:
+//  * int8_team_kernel (small batches): a workgroup owns 16 * RT rows of W and
+//    all of K, its waves take 256-code windows in turn and add their sums in
+//    LDS.  What bounds it is the weight stream from HBM, then the x rows every
+//    workgroup reads from L2.
+//  * int8_tile_kernel (larger ones): a workgroup owns BM rows of x and BN rows
+//    of W, both brought to LDS by its own loads a few stages ahead; K may be
+//    split between workgroups, the int32 partial tiles then go through the
+//    workspace to int8_reduce_kernel.  Bound by the matrix cores at long
+//    prompts.
+// Both bring W to LDS with loads that write LDS directly and whole 128-byte
+// lines per instruction where the weight stream is what counts.
+#include <type_traits>
+
+#include "int8_device.h"
 #include "launch.h"
 
 namespace sg {
@@ -15,74 +31,555 @@ namespace sg {
 namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+constexpr uint32_t kPastEnd = ~15u;  // buffer offset that reads zeros
 
 __device__ __forceinline__ i32x4_t mfma16(const uint4 w, const uint4 x, i32x4_t acc) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, w),
                                                  __builtin_bit_cast(i32x4_t, x), acc, 0, 0, 0);
 }
 
-__device__ __forceinline__ void store_scaled(const Int8Epilogue& ep, int64_t i, int acc, float ws,
-                                             float xs) {
-#pragma clang fp contract(off)  // the same roundings wherever an output is finished
-    float v = (float)acc * ws * xs;
-    if (ep.r) v += bf16_to_f32(ep.r[i]);
-    if (ep.y_f32) ep.y_f32[i] = v;
-    if (ep.y_bf16) ep.y_bf16[i] = f32_to_bf16(v);
+// 64 lanes x 16 bytes from the buffer (each lane its own offset) to 1 KB of LDS.
+template <int POLICY>
+__device__ __forceinline__ void load_to_lds(rsrc_t r, uint4* lds, uint32_t offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds, 16, (int)offset, 0, 0, POLICY);
 }
 
-// One wave: 16 rows of W times 16 * MT rows of x over all of K, both operands
-// straight from memory.
-template <int MT>
-__global__ __launch_bounds__(kBlock) void int8_direct_kernel(const int8_t* __restrict__ xq,
-                                                             const int8_t* __restrict__ wq, int M,
-                                                             int N, int K, Int8Epilogue ep) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int n0 = (blockIdx.x * kWavesPerBlock + wave_id_in_block()) * 16;
-    const int m0 = blockIdx.y * 16 * MT;
-    if (n0 >= N) return;
-    const int row = lane & 15, grp = lane >> 4;
-    const rsrc_t rw = make_rsrc(wq + (int64_t)n0 * K, (uint32_t)min(16, N - n0) * (uint32_t)K);
-    const rsrc_t rx = make_rsrc(xq + (int64_t)m0 * K, (uint32_t)min(16 * MT, M - m0) * (uint32_t)K);
-    i32x4_t acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = i32x4_t{0, 0, 0, 0};
-    for (int k0 = 0; k0 < K; k0 += 64) {
-        const int k = k0 + 16 * grp;
-        const bool in = k < K;  // K is a multiple of 16: a lane's codes are all in or all out
-        const uint4 w = load16(rw, in ? (uint32_t)row * K + k : ~15u);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const uint4 x = load16(rx, in ? (uint32_t)(16 * t + row) * K + k : ~15u);
-            acc[t] = mfma16(w, x, acc[t]);
+// y of four neighbouring outputs: one rounding for the conversion and each product
+__device__ __forceinline__ void scale4(const i32x4_t acc, const float4 ws, float xs, float (&y)[4]) {
+#pragma clang fp contract(off)
+    y[0] = (float)acc[0] * ws.x * xs;
+    y[1] = (float)acc[1] * ws.y * xs;
+    y[2] = (float)acc[2] * ws.z * xs;
+    y[3] = (float)acc[3] * ws.w * xs;
+}
+
+// Outputs y[m][n .. n+4) with the residual; rows of a multiple of 4 elements
+// keep the four together.
+__device__ __forceinline__ void finish4(const Int8Epilogue& ep, int N, int m, int n, float (&y)[4]) {
+    const int64_t at = (int64_t)m * N + n;
+    if ((N & 3) == 0) {
+        if (ep.r) {
+            const uint2 r = *reinterpret_cast<const uint2*>(ep.r + at);
+            y[0] = as_f(r.x << 16) + y[0];
+            y[1] = as_f(r.x & 0xffff0000u) + y[1];
+            y[2] = as_f(r.y << 16) + y[2];
+            y[3] = as_f(r.y & 0xffff0000u) + y[3];
         }
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int m = m0 + 16 * t + row;
-        if (m >= M) continue;
-        const float xs = ep.xs[m];
+        if (ep.y_f32)
+            *reinterpret_cast<float4*>(ep.y_f32 + at) = make_float4(y[0], y[1], y[2], y[3]);
+        if (ep.y_bf16)
+            *reinterpret_cast<uint2*>(ep.y_bf16 + at) =
+                make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+    } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            const int n = n0 + 4 * grp + v;
-            if (n < N) store_scaled(ep, (int64_t)m * N + n, acc[t][v], ep.ws[n], xs);
+            if (n + v >= N) break;
+            float o = y[v];
+            if (ep.r) o = bf16_to_f32(ep.r[at + v]) + o;
+            if (ep.y_f32) ep.y_f32[at + v] = o;
+            if (ep.y_bf16) ep.y_bf16[at + v] = f32_to_bf16(o);
         }
     }
+}
+
+// scales of channels n .. n+4 (zeros past N)
+__device__ __forceinline__ float4 channel_scales(const float* ws, int N, int n) {
+    if (n + 4 <= N) return make_float4(ws[n], ws[n + 1], ws[n + 2], ws[n + 3]);
+    return make_float4(n < N ? ws[n] : 0.0f, n + 1 < N ? ws[n + 1] : 0.0f,
+                       n + 2 < N ? ws[n + 2] : 0.0f, 0.0f);
+}
+
+// ---------------------------------------------------------------- team kernel
+
+// S waves share 16 * RT rows of W; wave s takes the 256-code windows s, s + S,
+// ... of K.  Each wave has two windows of W in flight in LDS slots of its own
+// (no barrier until the sums meet); the x codes of a window go straight to
+// registers.  A load instruction covers 4 rows x 256 bytes; the 16-byte piece p
+// of row r sits at place p ^ r of the row, so that reading one piece of 16
+// rows meets every bank once.
+template <int S, int RT, int MT>
+__global__ __launch_bounds__(S* kWave) void int8_team_kernel(const int8_t* __restrict__ xq,
+                                                             const int8_t* __restrict__ wq, int M,
+                                                             int N, int K, Int8Epilogue ep) {
+    static_assert(MT <= 4, "a wave's sums reuse its first LDS slot");
+    constexpr int kWin = 256;
+    __shared__ uint4 slot0[S][kWin * RT], slot1[S][kWin * RT];
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id_in_block();
+    const int row = lane & 15, grp = lane >> 4;
+    const int n0 = blockIdx.x * 16 * RT;
+    const rsrc_t rw = make_rsrc(wq + (int64_t)n0 * K, (uint32_t)min(16 * RT, N - n0) * (uint32_t)K);
+    const rsrc_t rx = make_rsrc(xq, (uint32_t)M * (uint32_t)K);
+
+    i32x4_t acc[RT][MT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+    uint4 x0[MT][4], x1[MT][4];
+    auto load = [&](int round, uint4* slot, uint4 (&x)[MT][4]) {
+        const int k = (round * S + wave) * kWin;
+#pragma unroll
+        for (int i = 0; i < 4 * RT; ++i) {
+            const int r = 4 * i + grp, kk = k + ((row ^ (r & 15)) * 16);
+            load_to_lds<kStream>(rw, slot + i * kWave, kk < K ? (uint32_t)r * K + kk : kPastEnd);
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int kk = k + t * 64 + grp * 16;
+                x[j][t] = load16(rx, kk < K ? (uint32_t)(16 * j + row) * K + kk : kPastEnd);
+            }
+    };
+    auto multiply = [&](const uint4* slot, const uint4 (&x)[MT][4]) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const uint4 w = slot[i * kWin + row * 16 + ((t * 4 + grp) ^ row)];
+#pragma unroll
+                for (int j = 0; j < MT; ++j) acc[i][j] = mfma16(w, x[j][t], acc[i][j]);
+            }
+    };
+    const int rounds = max(1, (K + kWin * S - 1) / (kWin * S));  // every load issued is used
+    load(0, slot0[wave], x0);
+    load(1, slot1[wave], x1);
+    for (int r = 0; r < rounds; r += 2) {
+        const bool more = r + 2 < rounds;
+        multiply(slot0[wave], x0);
+        if (more) load(r + 2, slot0[wave], x0);
+        multiply(slot1[wave], x1);
+        if (more) load(r + 3, slot1[wave], x1);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            slot0[wave][(i * MT + j) * kWave + lane] = __builtin_bit_cast(uint4, acc[i][j]);
+    __syncthreads();
+    for (int e = threadIdx.x; e < RT * MT * kWave; e += S * kWave) {
+        const int f = e >> 6, l = e & 63;
+        const int m = (f % MT) * 16 + (l & 15), n = n0 + (f / MT) * 16 + 4 * (l >> 4);
+        if (m >= M || n >= N) continue;
+        i32x4_t a = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < S; ++s) a += __builtin_bit_cast(i32x4_t, slot0[s][e]);
+        float y[4];
+        scale4(a, channel_scales(ep.ws, N, n), ep.xs[m], y);
+        finish4(ep, N, m, n, y);
+    }
+}
+
+// ---------------------------------------------------------------- tile kernel
+
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+    // at most N loads of this wave outstanding, its LDS reads done, then all waves
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
+}
+
+// FM + FN LDS reads spread over the FM * FN products of a step: the reads of the
+// next step's operands overlap the products of this one.
+template <int I, int FM, int FN>
+__device__ __forceinline__ void interleave() {
+    if constexpr (I < FM) {
+        constexpr int kReads = (FM + FN) * (I + 1) / FM - (FM + FN) * I / FM;
+        __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);  // LDS reads
+        __builtin_amdgcn_sched_group_barrier(0x8, FN, 0);        // matrix instructions
+        interleave<I + 1, FM, FN>();
+    }
+}
+
+enum TileOut { kTileFinal, kTilePartial, kTileGated };
+
+// A stage is 128 codes of K: a whole line of every row, two matrix steps.
+constexpr int kStageK = 128;
+constexpr int kPieces = kStageK / 16;     // 16-byte pieces of a row
+constexpr int kRowsPerLoad = 1024 / kStageK;  // a load instruction is 1 KB
+
+// Geometry of a tile variant: WM x WN waves, each FM 16-row tiles of x times FN
+// of W; NB stage buffers.
+template <int WM_, int WN_, int FM_, int FN_, int NB_>
+struct TileShape {
+    static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, NB = NB_;
+    static constexpr int W = WM * WN, BM = WM * FM * 16, BN = WN * FN * 16;
+    static constexpr int LX = BM / kRowsPerLoad / W, LW = BN / kRowsPerLoad / W;
+    static_assert(LX * kRowsPerLoad * W == BM && LW * kRowsPerLoad * W == BN, "whole loads a wave");
+    static_assert(NB >= 2 && NB <= 4, "two to four stage buffers");
+    static constexpr int kStage = (BM + BN) * kPieces;  // 16-byte pieces
+};
+
+template <class T, int OUT>
+__global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kernel(
+    const int8_t* __restrict__ xq, const int8_t* __restrict__ wq, int M, int N, int K, int tiles,
+    int per_xcd, int group, int kc, int32_t* partial, Int8Epilogue ep) {
+    constexpr int BM = T::BM, BN = T::BN, NB = T::NB, FM = T::FM, FN = T::FN, P = kPieces;
+    __shared__ uint4 b0[T::kStage], b1[T::kStage], b2[NB > 2 ? T::kStage : 1],
+        b3[NB > 3 ? T::kStage : 1];
+    __shared__ float sx[BM], sw[BN];
+    // Workgroups reach the 8 XCDs in turn: each XCD takes a run of consecutive
+    // tiles, and a run goes down `group` tiles of x before the next tile of W,
+    // so the tiles in flight on an XCD share rows of both through its L2.
+    const int t = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
+    if ((int)(blockIdx.x / kXcds) >= per_xcd || t >= tiles) return;
+    // a gated tile is BN / 2 outputs wide: 16 gate rows, then their 16 up rows
+    constexpr int BC = OUT == kTileGated ? BN / 2 : BN;
+    const int nn = (N + BC - 1) / BC, nm = (M + BM - 1) / BM;
+    const int first = t / (group * nn) * group, in = t - first * nn;
+    const int rows = min(group, nm - first);
+    const int m0 = (first + in % rows) * BM, n0 = in / rows * BC;
+    const int kbeg = blockIdx.y * kc, kend = min(K, kbeg + kc);
+
+    const int lane = threadIdx.x & (kWave - 1), w = wave_id_in_block();
+    const rsrc_t rx = make_rsrc(xq + (int64_t)m0 * K, (uint32_t)min(BM, M - m0) * (uint32_t)K);
+    const uint32_t wbytes = (uint32_t)min(BC, N - n0) * (uint32_t)K;
+    const rsrc_t rw = make_rsrc(wq + (int64_t)n0 * K, wbytes);
+    const rsrc_t ru = make_rsrc(wq + ((int64_t)n0 + (OUT == kTileGated ? N : 0)) * K, wbytes);
+    if constexpr (OUT != kTilePartial) {
+        for (int i = threadIdx.x; i < BM; i += T::W * kWave) sx[i] = m0 + i < M ? ep.xs[m0 + i] : 0.0f;
+        for (int i = threadIdx.x; i < BN; i += T::W * kWave) {
+            if constexpr (OUT == kTileGated) {
+                const int c = n0 + i / 32 * 16 + i % 16;
+                sw[i] = c < N ? ep.ws[c + (i % 32 >= 16 ? N : 0)] : 0.0f;
+            } else {
+                sw[i] = n0 + i < N ? ep.ws[n0 + i] : 0.0f;
+            }
+        }
+    }
+    // Piece p of row r sits at place p ^ (r % 8) of the row: 8 neighbouring rows
+    // of one piece meet every bank once.
+    const int lrow = lane / P, kpos = ((lane % P) ^ lrow) * 16;
+    uint32_t ox[T::LX], ow[T::LW];
+    bool up[T::LW];
+#pragma unroll
+    for (int i = 0; i < T::LX; ++i)
+        ox[i] = (uint32_t)((w * T::LX + i) * kRowsPerLoad + lrow) * K + kpos + kbeg;
+#pragma unroll
+    for (int i = 0; i < T::LW; ++i) {
+        int r = (w * T::LW + i) * kRowsPerLoad;
+        up[i] = OUT == kTileGated && r % 32 >= 16;
+        if constexpr (OUT == kTileGated) r = r / 32 * 16 + r % 16;
+        ow[i] = (uint32_t)(r + lrow) * K + kpos + kbeg;
+    }
+    const int klen = kend - kbeg - kpos;
+    auto issue = [&](uint4* b, int k0) {
+        const bool ok = k0 < klen;
+#pragma unroll
+        for (int i = 0; i < T::LX; ++i)
+            load_to_lds<kCached>(rx, b + (w * T::LX + i) * kWave, ok ? ox[i] + k0 : kPastEnd);
+#pragma unroll
+        for (int i = 0; i < T::LW; ++i)
+            load_to_lds<kCached>(up[i] ? ru : rw, b + BM * P + (w * T::LW + i) * kWave,
+                                 ok ? ow[i] + k0 : kPastEnd);
+    };
+
+    i32x4_t acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+    const int row = lane & 15, grp = lane >> 4, wm = w / T::WN, wn = w % T::WN;
+    const int xbase = (wm * FM * 16 + row) * P, wbase = (BM + wn * FN * 16 + row) * P;
+    uint4 fw[2][FN], fx[2][FM];
+    auto read = [&](const uint4* b, auto step, auto reg) {
+        constexpr int R = decltype(reg)::value;
+        const int p = (decltype(step)::value * 4 + grp) ^ (row & 7);
+#pragma unroll
+        for (int i = 0; i < FN; ++i) fw[R][i] = b[wbase + i * 16 * P + p];
+#pragma unroll
+        for (int j = 0; j < FM; ++j) fx[R][j] = b[xbase + j * 16 * P + p];
+    };
+    auto multiply = [&](auto reg) {
+        constexpr int R = decltype(reg)::value;
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+#pragma unroll
+            for (int i = 0; i < FN; ++i) acc[i][j] = mfma16(fw[R][i], fx[R][j], acc[i][j]);
+    };
+    std::integral_constant<int, 0> c0;
+    std::integral_constant<int, 1> c1;
+
+    // Stage s: wait until it has landed for every wave, refill the buffer of
+    // stage s - 1 (all its reads are done) with stage s + NB - 1, read its
+    // operands while the previous step's products run.
+    constexpr int kLoads = T::LX + T::LW;
+    const int n = max(1, (kend - kbeg + kStageK - 1) / kStageK);
+    auto stage = [&](const uint4* b, uint4* refill, int s) {
+        wait_and_barrier<(NB - 2) * kLoads>();
+        issue(refill, (s + NB - 1) * kStageK);
+        read(b, c0, c0);
+        multiply(c1);
+        interleave<0, FM, FN>();
+        read(b, c1, c1);
+        multiply(c0);
+        interleave<0, FM, FN>();
+    };
+    issue(b0, 0);
+    if constexpr (NB > 2) issue(b1, kStageK);
+    if constexpr (NB > 3) issue(b2, 2 * kStageK);
+    // stage 0: no products before it
+    wait_and_barrier<(NB - 2) * kLoads>();
+    issue(NB == 2 ? b1 : NB == 3 ? b2 : b3, (NB - 1) * kStageK);
+    read(b0, c0, c0);
+    read(b0, c1, c1);
+    multiply(c0);
+    int s = 1;
+    for (; s + NB <= n; s += NB) {
+        stage(b1, b0, s);
+        if constexpr (NB == 2) stage(b0, b1, s + 1);
+        if constexpr (NB > 2) stage(b2, b1, s + 1);
+        if constexpr (NB == 3) stage(b0, b2, s + 2);
+        if constexpr (NB > 3) stage(b3, b2, s + 2);
+        if constexpr (NB > 3) stage(b0, b3, s + 3);
+    }
+    if (s < n) stage(b1, b0, s);
+    if constexpr (NB > 2)
+        if (s + 1 < n) stage(b2, b1, s + 1);
+    if constexpr (NB > 3)
+        if (s + 2 < n) stage(b3, b2, s + 2);
+    multiply(c1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may outlive the workgroup's LDS
+
+    if constexpr (OUT == kTilePartial) {
+        int32_t* out = partial + ((int64_t)blockIdx.y * tiles + t) * (BM * BN);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+                if (m0 + (wm * FM + j) * 16 < M)
+                    reinterpret_cast<i32x4_t*>(out)[((w * FN + i) * FM + j) * kWave + lane] = acc[i][j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int ml = (wm * FM + j) * 16 + row, m = m0 + ml;
+            if (m >= M) continue;
+            const float xs = sx[ml];
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                const int nl = (wn * FN + i) * 16 + grp * 4;
+                float y[4];
+                if constexpr (OUT == kTileGated) {
+                    if (i % 2 == 0) {
+                        float u[4];
+                        const int c = n0 + nl / 32 * 16 + nl % 16;
+                        if (c >= N) continue;
+                        scale4(acc[i][j], *reinterpret_cast<const float4*>(&sw[nl]), xs, y);
+                        scale4(acc[i + 1][j], *reinterpret_cast<const float4*>(&sw[nl + 16]), xs, u);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) y[v] = gated_product(y[v], u[v]);
+                        *reinterpret_cast<float4*>(ep.y_f32 + (int64_t)m * N + c) =
+                            make_float4(y[0], y[1], y[2], y[3]);
+                    }
+                } else {
+                    if (n0 + nl >= N) continue;
+                    scale4(acc[i][j], *reinterpret_cast<const float4*>(&sw[nl]), xs, y);
+                    finish4(ep, N, m, n0 + nl, y);
+                }
+            }
+        }
+    }
+}
+
+// Sums the S partial tiles of int8_tile_kernel<T, kTilePartial> and finishes the
+// outputs; a thread owns the four neighbours a lane of the tile kernel held.
+template <class T>
+__global__ __launch_bounds__(kBlock) void int8_reduce_kernel(const int32_t* __restrict__ partial,
+                                                             int M, int N, int tiles, int group,
+                                                             int S, Int8Epilogue ep) {
+    constexpr int BM = T::BM, BN = T::BN, FM = T::FM, FN = T::FN;
+    constexpr int kFrags = T::W * FM * FN;  // 16 x 16 blocks of a tile
+    const int64_t e = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    const int t = (int)(e / (kFrags * kWave)), f = (int)(e / kWave) % kFrags, lane = (int)e & 63;
+    if (t >= tiles) return;
+    const int nn = (N + BN - 1) / BN, nm = (M + BM - 1) / BM;
+    const int first = t / (group * nn) * group, in = t - first * nn;
+    const int rows = min(group, nm - first);
+    const int m0 = (first + in % rows) * BM, n0 = in / rows * BN;
+    const int w = f / (FM * FN), i = f / FM % FN, j = f % FM;
+    const int m = m0 + ((w / T::WN) * FM + j) * 16 + (lane & 15);
+    const int n = n0 + ((w % T::WN) * FN + i) * 16 + (lane >> 4) * 4;
+    if (m >= M || n >= N) return;
+    const i32x4_t* p = reinterpret_cast<const i32x4_t*>(partial) +
+                       ((int64_t)t * kFrags + f) * kWave + lane;
+    const int64_t step = (int64_t)tiles * (BM * BN / 4);
+    i32x4_t a = {0, 0, 0, 0};
+    int s = 0;
+    for (; s + 4 <= S; s += 4) {
+        const i32x4_t q0 = p[s * step], q1 = p[(s + 1) * step], q2 = p[(s + 2) * step],
+                      q3 = p[(s + 3) * step];
+        a += (q0 + q1) + (q2 + q3);
+    }
+    for (; s < S; ++s) a += p[s * step];
+    float y[4];
+    scale4(a, channel_scales(ep.ws, N, n), ep.xs[m], y);
+    finish4(ep, N, m, n, y);
+}
+
+template <class T, int OUT>
+void launch_tile(int M, int N, int K, int S, int kc, int group, const int8_t* xq, const int8_t* wq,
+                 int32_t* partial, const Int8Epilogue& ep, hipStream_t stream) {
+    constexpr int BC = OUT == kTileGated ? T::BN / 2 : T::BN;
+    const int tiles = ((M + T::BM - 1) / T::BM) * ((N + BC - 1) / BC);
+    const int per = (tiles + kXcds - 1) / kXcds;
+    hipLaunchKernelGGL((int8_tile_kernel<T, OUT>), dim3(per * kXcds, S), dim3(T::W * kWave), 0,
+                       stream, xq, wq, M, N, K, tiles, per, group, kc, partial, ep);
+}
+
+template <class T>
+void launch_split(int M, int N, int K, int S, int kc, int group, const int8_t* xq, const int8_t* wq,
+                  void* ws, const Int8Epilogue& ep, hipStream_t stream) {
+    int32_t* partial = static_cast<int32_t*>(ws);
+    if (S <= 1) {
+        launch_tile<T, kTileFinal>(M, N, K, 1, K, group, xq, wq, nullptr, ep, stream);
+        return;
+    }
+    launch_tile<T, kTilePartial>(M, N, K, S, kc, group, xq, wq, partial, ep, stream);
+    const int tiles = ((M + T::BM - 1) / T::BM) * ((N + T::BN - 1) / T::BN);
+    const int64_t threads = (int64_t)tiles * (T::BM * T::BN / 4);
+    hipLaunchKernelGGL((int8_reduce_kernel<T>), dim3((uint32_t)((threads + kBlock - 1) / kBlock)),
+                       dim3(kBlock), 0, stream, partial, M, N, tiles, group, S, ep);
+}
+
+template <int S, int RT, int MT>
+void launch_team(int M, int N, int K, const int8_t* xq, const int8_t* wq, const Int8Epilogue& ep,
+                 hipStream_t stream) {
+    hipLaunchKernelGGL((int8_team_kernel<S, RT, MT>), dim3((N + 16 * RT - 1) / (16 * RT)),
+                       dim3(S * kWave), 0, stream, xq, wq, M, N, K, ep);
+}
+
+// ---------------------------------------------------------------- choice
+
+// Tile variants, BM x BN: 256 x 256, 128 x 256, 128 x 128, 64 x 128, 64 x 64.
+typedef TileShape<4, 2, 4, 8, 2> Tile256;
+typedef TileShape<2, 4, 4, 4, 3> Tile128w;
+typedef TileShape<2, 4, 4, 2, 4> Tile128;
+typedef TileShape<2, 2, 2, 4, 3> Tile64w;
+typedef TileShape<2, 2, 2, 2, 4> Tile64;
+
+template <class F>
+void with_tile(int v, F f) {
+    switch (v) {
+        case 0: f(Tile256{}); break;
+        case 1: f(Tile128w{}); break;
+        case 2: f(Tile128{}); break;
+        case 3: f(Tile64w{}); break;
+        default: f(Tile64{}); break;
+    }
+}
+
+struct TileCost {
+    int bm, bn;
+    int per_cu;      // workgroups a compute unit holds
+    int group;       // tiles of x an XCD's run goes down before the next tile of W
+    double full;     // ns per code of K of a round that fills every compute unit
+    double single;   // of a round with at most one workgroup a compute unit
+};
+// Measured on MI355X (full: 8192 x 8192 x 7168 and 1024..2048 x 4096 x 4096;
+// single: rounds of 64 to 256 tiles).
+constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.1, 10.4},
+                               {128, 256, 1, 8, 7.2, 6.2},
+                               {128, 128, 1, 8, 4.1, 3.9},
+                               {64, 128, 2, 8, 6.4, 3.6},
+                               {64, 64, 2, 8, 4.1, 2.6}};
+constexpr int kTileVariants = 5;
+constexpr int kCus = 256;
+constexpr int kTeamMaxM = 64;
+
+struct Int8Plan {
+    bool team;
+    int waves, rt;     // team kernel: waves a workgroup, 16-row tiles of W
+    int tile, S, kc;   // tile kernel: variant, K splits, codes a split
+    size_t workspace;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The variant with the least estimated time (us).  Team: 2 us, then 0.038 us
+// per KB of W and 0.018 per KB of x that a compute unit takes in.  Tiles: 3 us,
+// then rounds of workgroups at the measured cost per code; a split adds the
+// reduction's launch and its traffic.
+Int8Plan int8_plan(int M, int N, int K, bool tiles_only = false, bool one_split = false) {
+    Int8Plan best{};
+    double least = 1e30;
+    if (!tiles_only && M <= kTeamMaxM) {
+        for (int rt = 1; rt <= 2; ++rt) {
+            const double wgs = (double)ceil_div(N, 16 * rt);
+            const double per = wgs > kCus ? wgs / kCus : 1.0;
+            const double est = 2.0 + per * K * (0.038 * 16 * rt + 0.018 * M) / 1000.0;
+            if (est < least) {
+                least = est;
+                const int waves = K <= 1024 || rt == 2 || wgs >= 1.5 * kCus ? 4 : 8;
+                best = Int8Plan{true, waves, rt, 0, 1, K, 0};
+            }
+        }
+    }
+    for (int v = 0; v < kTileVariants; ++v) {
+        const TileCost& c = kTiles[v];
+        const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn);
+        for (int S = 1; S <= (one_split ? 1 : 16); ++S) {
+            const int kc = S == 1 ? K : (int)ceil_div(ceil_div(K, S), kStageK) * kStageK;
+            if (S > 1 && (kc < 4 * kStageK || (int64_t)(S - 1) * kc >= K)) break;
+            const int64_t wgs = tiles * S, slots = (int64_t)kCus * c.per_cu;
+            const int64_t rounds = wgs / slots, rem = wgs % slots;
+            const double tail = rem == 0 ? 0.0 : rem <= kCus ? c.single : c.full;
+            double est = 3.0 + kc * (rounds * c.full + tail) / 1000.0;
+            const size_t ws = S > 1 ? (size_t)S * tiles * c.bm * c.bn * 4 : 0;
+            if (S > 1) est += 3.0 + 8.0 * S * M * N / 4.0e6;
+            if (est < least && ws <= ((size_t)1 << 30)) {
+                least = est;
+                best = Int8Plan{false, 0, 0, v, S, kc, ws};
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
-size_t int8_workspace_bytes(int, int, int) { return 0; }
+size_t int8_workspace_bytes(int M, int N, int K) { return int8_plan(M, N, K).workspace; }
 
 hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t* wq,
-                            const Int8Epilogue& ep, void*, hipStream_t stream) {
-    const int gx = (N + 16 * kWavesPerBlock - 1) / (16 * kWavesPerBlock);
-    // grid.y: at most SG_INT8_MAX_M / 64 = 16384 tiles
-    if (M <= 16)
-        hipLaunchKernelGGL((int8_direct_kernel<1>), dim3(gx), dim3(kBlock), 0, stream, xq, wq, M, N,
-                           K, ep);
-    else
-        hipLaunchKernelGGL((int8_direct_kernel<4>), dim3(gx, (M + 63) / 64), dim3(kBlock), 0,
-                           stream, xq, wq, M, N, K, ep);
+                            const Int8Epilogue& ep, void* ws, hipStream_t stream) {
+    const Int8Plan p = int8_plan(M, N, K);
+    if (p.team) {
+        auto go = [&](auto mt) {
+            constexpr int MT = decltype(mt)::value;
+            if (p.rt == 2)
+                launch_team<4, 2, MT>(M, N, K, xq, wq, ep, stream);
+            else if (p.waves == 4)
+                launch_team<4, 1, MT>(M, N, K, xq, wq, ep, stream);
+            else
+                launch_team<8, 1, MT>(M, N, K, xq, wq, ep, stream);
+        };
+        if (M <= 16)
+            go(std::integral_constant<int, 1>{});
+        else if (M <= 32)
+            go(std::integral_constant<int, 2>{});
+        else
+            go(std::integral_constant<int, 4>{});
+    } else {
+        with_tile(p.tile, [&](auto shape) {
+            launch_split<decltype(shape)>(M, N, K, p.S, p.kc, kTiles[p.tile].group, xq, wq, ws, ep,
+                                          stream);
+        });
+    }
+    return hipGetLastError();
+}
+
+bool int8_gated_ok(int M, int F, int H) {
+    const Int8Plan p = int8_plan(M, 2 * F, H);
+    return !p.team && p.S == 1;
+}
+
+hipError_t launch_gated_int8(int M, int F, int H, const int8_t* xq, const int8_t* wq,
+                             const Int8Epilogue& ep, hipStream_t stream) {
+    const Int8Plan p = int8_plan(M, 2 * F, H, true, true);
+    with_tile(p.tile, [&](auto shape) {
+        launch_tile<decltype(shape), kTileGated>(M, F, H, 1, H, kTiles[p.tile].group, xq, wq,
+                                                 nullptr, ep, stream);
+    });
     return hipGetLastError();
 }
 

@@ -174,10 +174,20 @@ sg_status skinny_mlp_int8_step(const sg_mlp_int8_step* a, void* workspace, size_
     if ((st = skinny_rmsnorm(a->M, a->H, a->x, a->r, a->g, a->eps, a->out, nullptr, q, sq,
                              stream)) != SG_OK)
         return st;
-    if ((st = skinny_gemm_int8(a->M, 2 * a->F, a->H, q, sq, a->W_gate_up, a->gate_up_scales,
-                               nullptr, u, nullptr, gw, L.gemm_bytes, stream)) != SG_OK)
-        return st;
-    if ((st = skinny_quant_int8(a->M, a->F, nullptr, u, 1, p, sp, stream)) != SG_OK) return st;
+    if (sg::int8_gated_ok(a->M, a->F, a->H)) {
+        // long prompts: the gated product leaves the projection's epilogue, u is [M, F]
+        const sg::Int8Epilogue ep{sq, a->gate_up_scales, u, nullptr, nullptr};
+        if (sg::launch_gated_int8(a->M, a->F, a->H, q, a->W_gate_up, ep,
+                                  static_cast<hipStream_t>(stream)) != hipSuccess)
+            return SG_ERR_HIP;
+        sg::count_launch(SG_KERNEL_INT8);
+        st = skinny_quant_int8(a->M, a->F, nullptr, u, 0, p, sp, stream);
+    } else {
+        st = skinny_gemm_int8(a->M, 2 * a->F, a->H, q, sq, a->W_gate_up, a->gate_up_scales,
+                              nullptr, u, nullptr, gw, L.gemm_bytes, stream);
+        if (st == SG_OK) st = skinny_quant_int8(a->M, a->F, nullptr, u, 1, p, sp, stream);
+    }
+    if (st != SG_OK) return st;
     return skinny_gemm_int8(a->M, a->H, a->F, p, sp, a->W_down, a->down_scales, a->out, nullptr,
                             a->out, gw, L.gemm_bytes, stream);
 }

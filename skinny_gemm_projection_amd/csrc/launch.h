@@ -188,6 +188,13 @@ struct Int8Epilogue {
     const uint16_t* r;    // residual [M, N] or nullptr
 };
 size_t int8_workspace_bytes(int M, int N, int K);
+// The gated product in the epilogue of the gate and up projections: y_f32
+// [M, F] = silu(x Wg^T) * (x Wu^T) for wq [2F, H] (gate rows, then up rows) and
+// its scales, F a multiple of 16; where int8_gated_ok, the same bits as the
+// separate calls give.
+bool int8_gated_ok(int M, int F, int H);
+hipError_t launch_gated_int8(int M, int F, int H, const int8_t* xq, const int8_t* wq,
+                             const Int8Epilogue& ep, hipStream_t stream);
 hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t* wq,
                             const Int8Epilogue& ep, void* ws, hipStream_t stream);
 

@@ -18,6 +18,7 @@
 
 #include <type_traits>
 
+#include "int8_device.h"
 #include "launch.h"
 
 namespace sg {
@@ -26,14 +27,6 @@ namespace {
 
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: x + kMagic is x rounded to a whole number
 constexpr uint32_t kInfBits = 0x7f800000u;
-
-// bf16 pair of two fp32 values (round to nearest even), a in the low half
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    bf16x2_t p;
-    p[0] = (__bf16)a;
-    p[1] = (__bf16)b;
-    return __builtin_bit_cast(uint32_t, p);
-}
 
 __device__ __forceinline__ void unpack8(const uint4 u, float (&v)[8]) {
     const uint32_t d[4] = {u.x, u.y, u.z, u.w};
@@ -183,11 +176,6 @@ __global__ __launch_bounds__(THREADS* ROWS) void rmsnorm_kernel(
         const float m = store_codes<THREADS, P>(t, amax, bad, tid, n8, codes + row * K);
         if (tid == 0) scales[row] = m * inv / 127.0f;
     }
-}
-
-// silu(g) * u in fp32
-__device__ __forceinline__ float gated_product(float g, float u) {
-    return g / (1.0f + __expf(-g)) * u;
 }
 
 template <bool F32>
