@@ -33,7 +33,9 @@ namespace {
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 
-constexpr uint32_t kPastEnd = ~15u;  // buffer offset that reads zeros
+// A buffer offset that reads zeros, also after a row offset is added: buffers
+// here end below 2^31 and rows of one tile span less than 2^27 bytes.
+constexpr uint32_t kPastEnd = 1u << 31;
 
 __device__ __forceinline__ i32x4_t mfma16(const uint4 w, const uint4 x, i32x4_t acc) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, w),
@@ -180,15 +182,17 @@ __device__ __forceinline__ void wait_and_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
 }
 
-// FM + FN LDS reads spread over the FM * FN products of a step: the reads of the
-// next step's operands overlap the products of this one.
-template <int I, int FM, int FN>
+// Schedules one step: FM + FN LDS reads (the next step's operands) and LOADS
+// loads of a later stage, spread over the FM * FN products of this step.
+template <int I, int FM, int FN, int LOADS>
 __device__ __forceinline__ void interleave() {
     if constexpr (I < FM) {
         constexpr int kReads = (FM + FN) * (I + 1) / FM - (FM + FN) * I / FM;
+        constexpr int kLoads = LOADS * (I + 1) / FM - LOADS * I / FM;
+        if constexpr (kLoads > 0) __builtin_amdgcn_sched_group_barrier(0x10, kLoads, 0);  // loads
         __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);  // LDS reads
         __builtin_amdgcn_sched_group_barrier(0x8, FN, 0);        // matrix instructions
-        interleave<I + 1, FM, FN>();
+        interleave<I + 1, FM, FN, LOADS>();
     }
 }
 
@@ -251,28 +255,23 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
     // Piece p of row r sits at place p ^ (r % 8) of the row: 8 neighbouring rows
     // of one piece meet every bank once.
     const int lrow = lane / P, kpos = ((lane % P) ^ lrow) * 16;
-    uint32_t ox[T::LX], ow[T::LW];
-    bool up[T::LW];
-#pragma unroll
-    for (int i = 0; i < T::LX; ++i)
-        ox[i] = (uint32_t)((w * T::LX + i) * kRowsPerLoad + lrow) * K + kpos + kbeg;
-#pragma unroll
-    for (int i = 0; i < T::LW; ++i) {
-        int r = (w * T::LW + i) * kRowsPerLoad;
-        up[i] = OUT == kTileGated && r % 32 >= 16;
-        if constexpr (OUT == kTileGated) r = r / 32 * 16 + r % 16;
-        ow[i] = (uint32_t)(r + lrow) * K + kpos + kbeg;
-    }
+    const uint32_t lbase = (uint32_t)lrow * K + kpos + kbeg;
     const int klen = kend - kbeg - kpos;
+    // this lane's offset plus a scalar one for each load; past kend the lane reads zeros
     auto issue = [&](uint4* b, int k0) {
-        const bool ok = k0 < klen;
+        const uint32_t base = k0 < klen ? lbase : kPastEnd;
 #pragma unroll
-        for (int i = 0; i < T::LX; ++i)
-            load_to_lds<kCached>(rx, b + (w * T::LX + i) * kWave, ok ? ox[i] + k0 : kPastEnd);
+        for (int i = 0; i < T::LX; ++i) {
+            const int r = (w * T::LX + i) * kRowsPerLoad;
+            load_to_lds<kCached>(rx, b + r * P, base + (uint32_t)(r * K + k0));
+        }
 #pragma unroll
-        for (int i = 0; i < T::LW; ++i)
-            load_to_lds<kCached>(up[i] ? ru : rw, b + BM * P + (w * T::LW + i) * kWave,
-                                 ok ? ow[i] + k0 : kPastEnd);
+        for (int i = 0; i < T::LW; ++i) {
+            const int r = (w * T::LW + i) * kRowsPerLoad;
+            const bool up = OUT == kTileGated && r % 32 >= 16;
+            const int src = OUT == kTileGated ? r / 32 * 16 + r % 16 : r;
+            load_to_lds<kCached>(up ? ru : rw, b + (BM + r) * P, base + (uint32_t)(src * K + k0));
+        }
     };
 
     i32x4_t acc[FN][FM];
@@ -311,10 +310,10 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
         issue(refill, (s + NB - 1) * kStageK);
         read(b, c0, c0);
         multiply(c1);
-        interleave<0, FM, FN>();
+        interleave<0, FM, FN, kLoads>();
         read(b, c1, c1);
         multiply(c0);
-        interleave<0, FM, FN>();
+        interleave<0, FM, FN, 0>();
     };
     issue(b0, 0);
     if constexpr (NB > 2) issue(b1, kStageK);
@@ -452,7 +451,7 @@ void launch_team(int M, int N, int K, const int8_t* xq, const int8_t* wq, const 
 // ---------------------------------------------------------------- choice
 
 // Tile variants, BM x BN: 256 x 256, 128 x 256, 128 x 128, 64 x 128, 64 x 64.
-typedef TileShape<4, 2, 4, 8, 2> Tile256;
+typedef TileShape<2, 4, 8, 4, 2> Tile256;
 typedef TileShape<2, 4, 4, 4, 3> Tile128w;
 typedef TileShape<2, 4, 4, 2, 4> Tile128;
 typedef TileShape<2, 2, 2, 4, 3> Tile64w;
