@@ -347,7 +347,8 @@ def skinny_gemm_fp8(x: torch.Tensor, W_codes: torch.Tensor, W_scales: torch.Tens
 def _arg(t, dtype, shape, name, dev):
     """Device pointer of a contiguous tensor of exactly this type, shape and device."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev.index
+                and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:  # not a tensor: _ptr says so
         pass
@@ -360,17 +361,20 @@ def _opt(t, dtype, shape, name, dev):
 
 
 def _rows(x, name, dtypes):
-    """(rows, columns, device) of a 2-D device tensor of one of the types."""
+    """(rows, columns, device, pointer) of a contiguous 2-D device tensor of one of the types."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(x).__name__}")
     if x.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
     if not x.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
-    shape = x.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(shape)}")
-    return shape[0], shape[1], x.device
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    try:
+        M, K = x.shape
+    except ValueError:
+        raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(x.shape)}") from None
+    return M, K, x.device, x.data_ptr()
 
 
 def _new(shape, dtype, dev, stream):
@@ -416,14 +420,15 @@ def skinny_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, r=None, h=None,
     y_bf16 (bf16 [M, K], each may be x or r itself) and codes int8 [M, K] with scales float32 [M]
     (y is about codes * scales[:, None]); allocates codes and scales when neither y_bf16 nor codes
     is given, and scales when only codes is.  Returns (h, y_bf16, codes, scales)."""
-    M, K, dev = _rows(x, "x", (torch.bfloat16,))
+    bf16 = torch.bfloat16
+    M, K, dev, px = _rows(x, "x", (bf16,))
+    mk = (M, K)
     if codes is None and (y_bf16 is None or scales is not None):
         codes = _new((M, K), torch.int8, dev, stream)
     if codes is not None and scales is None:
         scales = _new((M,), torch.float32, dev, stream)
-    bf16, mk = torch.bfloat16, (M, K)
-    _run_on(dev, stream, _c().skinny_rmsnorm, M, K, _arg(x, bf16, mk, "x", dev),
-            _opt(r, bf16, mk, "r", dev), _arg(g, bf16, (K,), "g", dev), eps,
+    _run_on(dev, stream, _c().skinny_rmsnorm, M, K, px, _opt(r, bf16, mk, "r", dev),
+            _arg(g, bf16, (K,), "g", dev), eps,
             _opt(h, bf16, mk, "h", dev), _opt(y_bf16, bf16, mk, "y_bf16", dev),
             _opt(codes, torch.int8, mk, "codes", dev),
             _opt(scales, torch.float32, (M,), "scales", dev))
@@ -434,8 +439,7 @@ def skinny_quant_int8(x: torch.Tensor, gated: bool = False, codes=None, scales=N
     """Codes int8 [M, K] and scales float32 [M] of rows of x (bf16 or float32): of x [M, K]
     itself, or with gated of silu(x[:, :K]) * x[:, K:] for x [M, 2K].  Rows are tokens in front
     of an integer projection, or the channels of a weight matrix.  Returns (codes, scales)."""
-    M, K, dev = _rows(x, "x", (torch.bfloat16, torch.float32))
-    width = K
+    M, K, dev, px = _rows(x, "x", (torch.bfloat16, torch.float32))
     if gated:
         if K % 2:
             raise ValueError(f"x: gated rows hold gate and up halves, got {K} columns")
@@ -444,7 +448,6 @@ def skinny_quant_int8(x: torch.Tensor, gated: bool = False, codes=None, scales=N
         codes = _new((M, K), torch.int8, dev, stream)
     if scales is None:
         scales = _new((M,), torch.float32, dev, stream)
-    px = _arg(x, x.dtype, (M, width), "x", dev)
     f32 = x.dtype is torch.float32
     _run_on(dev, stream, _c().skinny_quant_int8, M, K, None if f32 else px, px if f32 else None,
             1 if gated else 0, _arg(codes, torch.int8, (M, K), "codes", dev),
@@ -466,14 +469,14 @@ def skinny_gemm_int8(x_codes: torch.Tensor, x_scales: torch.Tensor, W_codes: tor
     be r).  Allocates y_f32 when no output is given, and the workspace when one is needed and
     none is given; returns the outputs."""
     i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
-    M, K, dev = _rows(x_codes, "x_codes", (i8,))
-    N = _rows(W_codes, "W_codes", (i8,))[0]
+    M, K, dev, px = _rows(x_codes, "x_codes", (i8,))
+    N = W_codes.shape[0]
     mn = (M, N)
     c = _c()
     if y_f32 is None and y_bf16 is None:
         y_f32 = _new(mn, torch.float32, dev, stream)
     ws, ws_ptr, ws_bytes = _ws_arg(workspace, c.skinny_gemm_int8_workspace(M, N, K), dev, stream)
-    _run_on(dev, stream, c.skinny_gemm_int8, M, N, K, _arg(x_codes, i8, (M, K), "x_codes", dev),
+    _run_on(dev, stream, c.skinny_gemm_int8, M, N, K, px,
             _arg(x_scales, f32, (M,), "x_scales", dev), _arg(W_codes, i8, (N, K), "W_codes", dev),
             _arg(W_scales, f32, (N,), "W_scales", dev),
             None if r is None else _arg(r, bf16, mn, "r", dev),
@@ -494,7 +497,7 @@ def skinny_mlp_int8_step(x: torch.Tensor, g: torch.Tensor, eps: float, W_gate_up
     the norm's output and the gated product quantised a token at a time.  x, r [M, H], g [H] bf16;
     W_gate_up int8 [2F, H] (gate rows, then up rows), W_down int8 [H, F], float32 scales per row.
     out bf16 [M, H] (may be x or r itself; allocated when not given).  Returns out."""
-    M, H, dev = _rows(x, "x", (torch.bfloat16,))
+    M, H, dev, px = _rows(x, "x", (torch.bfloat16,))
     F = _rows(W_down, "W_down", (torch.int8,))[1]
     if out is None:
         out = _new((M, H), torch.bfloat16, dev, stream)
@@ -502,8 +505,7 @@ def skinny_mlp_int8_step(x: torch.Tensor, g: torch.Tensor, eps: float, W_gate_up
                                    stream)
     i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
     step = SgMlpInt8Step(
-        _arg(x, bf16, (M, H), "x", dev), _opt(r, bf16, (M, H), "r", dev),
-        _arg(g, bf16, (H,), "g", dev), _arg(W_gate_up, i8, (2 * F, H), "W_gate_up", dev),
+        px, _opt(r, bf16, (M, H), "r", dev), _arg(g, bf16, (H,), "g", dev), _arg(W_gate_up, i8, (2 * F, H), "W_gate_up", dev),
         _arg(gate_up_scales, f32, (2 * F,), "gate_up_scales", dev),
         _arg(W_down, i8, (H, F), "W_down", dev), _arg(down_scales, f32, (H,), "down_scales", dev),
         _arg(out, bf16, (M, H), "out", dev), M, H, F, eps)
