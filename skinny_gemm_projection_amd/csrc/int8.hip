@@ -223,6 +223,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
     __shared__ uint4 b0[T::kStage], b1[T::kStage], b2[NB > 2 ? T::kStage : 1],
         b3[NB > 3 ? T::kStage : 1];
     __shared__ float sx[BM], sw[BN];
+    __shared__ uint32_t touched[T::W][kWave];  // where the touching loads land; never read
     // Workgroups reach the 8 XCDs in turn: each XCD takes a run of consecutive
     // tiles, and a run goes down `group` tiles of x before the next tile of W,
     // so the tiles in flight on an XCD share rows of both through its L2.
@@ -274,6 +275,31 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
         }
     };
 
+    // With two buffers a stage is requested only one stage ahead, less than a
+    // miss to HBM takes under load.  So every wave also reads one word of some
+    // lines of the stage kAhead ahead, which brings them to L2: the workgroups
+    // an XCD runs at once share rows (kShareW tiles of x along a tile of W,
+    // kShareX the other way) and touch one part each.  On inputs larger than the
+    // caches 8192 x 8192 x 7168 takes 359 against 383 us without, 1536 x 7168 x
+    // 18432 183 against 219; with three or four buffers it cost 5 to 10 %.
+    constexpr bool kTouch = NB == 2;
+    constexpr int kAhead = 4, kShareX = 8, kShareW = 4, kTouches = kTouch ? 2 : 0;
+    constexpr int kLinesX = BM / kShareX / T::W, kLinesW = BN / kShareW / T::W;  // a wave's
+    const uint32_t tx = lane < kLinesX ? (uint32_t)((n0 / BC % kShareX * T::W + w) * kLinesX + lane) * K + kbeg
+                                       : kPastEnd;
+    const uint32_t tw = lane < kLinesW ? (uint32_t)((m0 / BM % kShareW * T::W + w) * kLinesW + lane) * K + kbeg
+                                       : kPastEnd;
+    auto touch = [&](int stage) {
+        if constexpr (kTouch) {
+            const int k0 = (stage + kAhead) * kStageK;
+            const bool ok = k0 < kend - kbeg;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)touched[w], 4,
+                                                     (int)(ok ? tw + k0 : kPastEnd), 0, 0, kCached);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)touched[w], 4,
+                                                     (int)(ok ? tx + k0 : kPastEnd), 0, 0, kCached);
+        }
+    };
+
     i32x4_t acc[FN][FM];
 #pragma unroll
     for (int i = 0; i < FN; ++i)
@@ -302,25 +328,29 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
 
     // Stage s: wait until it has landed for every wave, refill the buffer of
     // stage s - 1 (all its reads are done) with stage s + NB - 1, read its
-    // operands while the previous step's products run.
-    constexpr int kLoads = T::LX + T::LW;
+    // operands while the previous step's products run.  (Loads return in order:
+    // the touching loads of a stage are behind its refill and may be out yet.)
+    constexpr int kLoads = T::LX + T::LW, kOut = (NB - 2) * kLoads + kTouches;
     const int n = max(1, (kend - kbeg + kStageK - 1) / kStageK);
     auto stage = [&](const uint4* b, uint4* refill, int s) {
-        wait_and_barrier<(NB - 2) * kLoads>();
+        wait_and_barrier<kOut>();
         issue(refill, (s + NB - 1) * kStageK);
+        touch(s);
         read(b, c0, c0);
         multiply(c1);
-        interleave<0, FM, FN, kLoads>();
+        interleave<0, FM, FN, kLoads + kTouches>();
         read(b, c1, c1);
         multiply(c0);
         interleave<0, FM, FN, 0>();
     };
     issue(b0, 0);
+    touch(-1);
     if constexpr (NB > 2) issue(b1, kStageK);
     if constexpr (NB > 3) issue(b2, 2 * kStageK);
     // stage 0: no products before it
-    wait_and_barrier<(NB - 2) * kLoads>();
+    wait_and_barrier<kOut>();
     issue(NB == 2 ? b1 : NB == 3 ? b2 : b3, (NB - 1) * kStageK);
+    touch(0);
     read(b0, c0, c0);
     read(b0, c1, c1);
     multiply(c0);
@@ -477,7 +507,7 @@ struct TileCost {
 };
 // Measured on MI355X (full: 8192 x 8192 x 7168 and 1024..2048 x 4096 x 4096;
 // single: rounds of 64 to 256 tiles).
-constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.1, 10.4},
+constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.0, 9.9},
                                {128, 256, 1, 8, 7.2, 6.2},
                                {128, 128, 1, 8, 4.1, 3.9},
                                {64, 128, 2, 8, 6.4, 3.6},
