@@ -93,21 +93,44 @@ __device__ __forceinline__ float4 channel_scales(const float* ws, int N, int n) 
                        n + 2 < N ? ws[n + 2] : 0.0f, 0.0f);
 }
 
-// ---------------------------------------------------------------- team kernel
+// ---------------------------------------------------------------- team kernels
 
-// S waves share 16 * RT rows of W; wave s takes the 256-code windows s, s + S,
-// ... of K.  Each wave has two windows of W in flight in LDS slots of its own
-// (no barrier until the sums meet); the x codes of a window go straight to
-// registers.  A load instruction covers 4 rows x 256 bytes; the 16-byte piece p
-// of row r sits at place p ^ r of the row, so that reading one piece of 16
-// rows meets every bank once.
+// Sums of the S waves of a workgroup (RT * MT blocks of 16 x 16 each, in the
+// LDS at sums + wave * stride) and the finished outputs.
 template <int S, int RT, int MT>
+__device__ __forceinline__ void finish_team(const uint4* sums, int stride, int M, int N, int n0,
+                                            const Int8Epilogue& ep) {
+    for (int e = threadIdx.x; e < RT * MT * kWave; e += S * kWave) {
+        const int f = e >> 6, l = e & 63;
+        const int m = (f % MT) * 16 + (l & 15), n = n0 + (f / MT) * 16 + 4 * (l >> 4);
+        if (m >= M || n >= N) continue;
+        i32x4_t a = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < S; ++s) a += __builtin_bit_cast(i32x4_t, sums[s * stride + e]);
+        float y[4];
+        scale4(a, channel_scales(ep.ws, N, n), ep.xs[m], y);
+        finish4(ep, N, m, n, y);
+    }
+}
+
+// S waves share 16 * RT rows of W and all of x; wave s takes the 128-code
+// windows s, s + S, ... of K, D of them in flight, W and x both in LDS slots of
+// the wave's own: no barrier until the sums meet.  A load instruction covers 8
+// rows x 128 bytes, whole lines: with 64 bytes of 16 rows, the layout of the
+// operand registers, reading W alone took 15 to 25 % longer (7168 x 8192 13.2
+// against 10.7 us), and x came from L2 at 30 against 43 bytes a clock.  The
+// 16-byte piece p of row r sits at place p ^ (r % 8) of the row.  W carries the
+// non-temporal hint.
+template <int S, int RT, int MT, int D>
 __global__ __launch_bounds__(S* kWave) void int8_team_kernel(const int8_t* __restrict__ xq,
                                                              const int8_t* __restrict__ wq, int M,
                                                              int N, int K, Int8Epilogue ep) {
-    static_assert(MT <= 4, "a wave's sums reuse its first LDS slot");
-    constexpr int kWin = 256;
-    __shared__ uint4 slot0[S][kWin * RT], slot1[S][kWin * RT];
+    static_assert(D == 2 || D == 4, "two or four slots");
+    constexpr int kWin = 128, P = kWin / 16, kRows = 1024 / kWin;
+    constexpr int kSlot = 16 * (RT + MT) * P;
+    static_assert(kSlot >= RT * MT * kWave, "a wave's sums reuse its first slot");
+    __shared__ uint4 slot0[S][kSlot], slot1[S][kSlot];
+    __shared__ uint4 slot2[D > 2 ? S : 1][D > 2 ? kSlot : 1], slot3[D > 2 ? S : 1][D > 2 ? kSlot : 1];
     const int lane = threadIdx.x & (kWave - 1), wave = wave_id_in_block();
     const int row = lane & 15, grp = lane >> 4;
     const int n0 = blockIdx.x * 16 * RT;
@@ -119,31 +142,93 @@ __global__ __launch_bounds__(S* kWave) void int8_team_kernel(const int8_t* __res
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
-    uint4 x0[MT][4], x1[MT][4];
-    auto load = [&](int round, uint4* slot, uint4 (&x)[MT][4]) {
+    const int lrow = lane / P, kpos = ((lane % P) ^ lrow) * 16;
+    auto load = [&](int round, uint4* slot) {
+        const int k = (round * S + wave) * kWin + kpos;
+        const uint32_t at = k < K ? (uint32_t)lrow * K + k : kPastEnd;
+#pragma unroll
+        for (int i = 0; i < 16 * RT / kRows; ++i)
+            load_to_lds<kStream>(rw, slot + i * kWave, at + (uint32_t)(i * kRows * K));
+#pragma unroll
+        for (int i = 0; i < 16 * MT / kRows; ++i)
+            load_to_lds<kCached>(rx, slot + 16 * RT * P + i * kWave, at + (uint32_t)(i * kRows * K));
+    };
+    auto multiply = [&](const uint4* slot) {
+#pragma unroll
+        for (int t = 0; t < kWin / 64; ++t) {
+            const int p = (t * 4 + grp) ^ (row & 7);
+            uint4 w[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) w[i] = slot[(i * 16 + row) * P + p];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const uint4 x = slot[((RT + j) * 16 + row) * P + p];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) acc[i][j] = mfma16(w[i], x, acc[i][j]);
+            }
+        }
+    };
+    const int rounds = max(1, (K + kWin * S - 1) / (kWin * S));  // every load issued is used
+    load(0, slot0[wave]);
+    load(1, slot1[wave]);
+    if constexpr (D > 2) load(2, slot2[wave]), load(3, slot3[wave]);
+    for (int r = 0; r < rounds; r += D) {
+        const bool more = r + D < rounds;
+        multiply(slot0[wave]);
+        if (more) load(r + D, slot0[wave]);
+        multiply(slot1[wave]);
+        if (more) load(r + D + 1, slot1[wave]);
+        if constexpr (D > 2) {
+            multiply(slot2[wave]);
+            if (more) load(r + D + 2, slot2[wave]);
+            multiply(slot3[wave]);
+            if (more) load(r + D + 3, slot3[wave]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            slot0[wave][(i * MT + j) * kWave + lane] = __builtin_bit_cast(uint4, acc[i][j]);
+    __syncthreads();
+    finish_team<S, RT, MT>(slot0[0], kSlot, M, N, n0, ep);
+}
+
+// The same for a few rows of x and very wide W (many workgroups a compute
+// unit): x goes straight to the operand registers, which leaves the LDS to W,
+// in 256-code windows, and twice as many workgroups resident.  4 x 36864 x 7168
+// takes 40.0 us against 44.1 with x in LDS, 5 x 7820 x 3696 7.6 against 8.7; at
+// 8192 x 7168 the other form is as fast, at 4096 rows of W faster.
+template <int S>
+__global__ __launch_bounds__(S* kWave) void int8_wide_kernel(const int8_t* __restrict__ xq,
+                                                             const int8_t* __restrict__ wq, int M,
+                                                             int N, int K, Int8Epilogue ep) {
+    constexpr int kWin = 256;
+    __shared__ uint4 slot0[S][kWin], slot1[S][kWin];
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id_in_block();
+    const int row = lane & 15, grp = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    const rsrc_t rw = make_rsrc(wq + (int64_t)n0 * K, (uint32_t)min(16, N - n0) * (uint32_t)K);
+    const rsrc_t rx = make_rsrc(xq, (uint32_t)M * (uint32_t)K);
+
+    i32x4_t acc = {0, 0, 0, 0};
+    uint4 x0[4], x1[4];
+    auto load = [&](int round, uint4* slot, uint4 (&x)[4]) {
         const int k = (round * S + wave) * kWin;
 #pragma unroll
-        for (int i = 0; i < 4 * RT; ++i) {
-            const int r = 4 * i + grp, kk = k + ((row ^ (r & 15)) * 16);
+        for (int i = 0; i < 4; ++i) {  // 4 rows x 256 bytes, piece p of row r at place p ^ r
+            const int r = 4 * i + grp, kk = k + ((row ^ r) * 16);
             load_to_lds<kStream>(rw, slot + i * kWave, kk < K ? (uint32_t)r * K + kk : kPastEnd);
         }
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int kk = k + t * 64 + grp * 16;
-                x[j][t] = load16(rx, kk < K ? (uint32_t)(16 * j + row) * K + kk : kPastEnd);
-            }
+        for (int t = 0; t < 4; ++t) {
+            const int kk = k + t * 64 + grp * 16;
+            x[t] = load16(rx, kk < K ? (uint32_t)row * K + kk : kPastEnd);
+        }
     };
-    auto multiply = [&](const uint4* slot, const uint4 (&x)[MT][4]) {
+    auto multiply = [&](const uint4* slot, const uint4 (&x)[4]) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const uint4 w = slot[i * kWin + row * 16 + ((t * 4 + grp) ^ row)];
-#pragma unroll
-                for (int j = 0; j < MT; ++j) acc[i][j] = mfma16(w, x[j][t], acc[i][j]);
-            }
+        for (int t = 0; t < 4; ++t) acc = mfma16(slot[row * 16 + ((t * 4 + grp) ^ row)], x[t], acc);
     };
     const int rounds = max(1, (K + kWin * S - 1) / (kWin * S));  // every load issued is used
     load(0, slot0[wave], x0);
@@ -155,23 +240,9 @@ __global__ __launch_bounds__(S* kWave) void int8_team_kernel(const int8_t* __res
         multiply(slot1[wave], x1);
         if (more) load(r + 3, slot1[wave], x1);
     }
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-            slot0[wave][(i * MT + j) * kWave + lane] = __builtin_bit_cast(uint4, acc[i][j]);
+    slot0[wave][lane] = __builtin_bit_cast(uint4, acc);
     __syncthreads();
-    for (int e = threadIdx.x; e < RT * MT * kWave; e += S * kWave) {
-        const int f = e >> 6, l = e & 63;
-        const int m = (f % MT) * 16 + (l & 15), n = n0 + (f / MT) * 16 + 4 * (l >> 4);
-        if (m >= M || n >= N) continue;
-        i32x4_t a = {0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < S; ++s) a += __builtin_bit_cast(i32x4_t, slot0[s][e]);
-        float y[4];
-        scale4(a, channel_scales(ep.ws, N, n), ep.xs[m], y);
-        finish4(ep, N, m, n, y);
-    }
+    finish_team<S, 1, 1>(slot0[0], kWin, M, N, n0, ep);
 }
 
 // ---------------------------------------------------------------- tile kernel
@@ -196,6 +267,14 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
+template <int I, int END, class F>
+__device__ __forceinline__ void unrolled(F f) {
+    if constexpr (I < END) {
+        f(std::integral_constant<int, I>{});
+        unrolled<I + 1, END>(f);
+    }
+}
+
 enum TileOut { kTileFinal, kTilePartial, kTileGated };
 
 // A stage is 128 codes of K: a whole line of every row, two matrix steps.
@@ -211,7 +290,7 @@ struct TileShape {
     static constexpr int W = WM * WN, BM = WM * FM * 16, BN = WN * FN * 16;
     static constexpr int LX = BM / kRowsPerLoad / W, LW = BN / kRowsPerLoad / W;
     static_assert(LX * kRowsPerLoad * W == BM && LW * kRowsPerLoad * W == BN, "whole loads a wave");
-    static_assert(NB >= 2 && NB <= 4, "two to four stage buffers");
+    static_assert(NB >= 2 && NB <= 8, "two to eight stage buffers");
     static constexpr int kStage = (BM + BN) * kPieces;  // 16-byte pieces
 };
 
@@ -220,8 +299,22 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
     const int8_t* __restrict__ xq, const int8_t* __restrict__ wq, int M, int N, int K, int tiles,
     int per_xcd, int group, int kc, int32_t* partial, Int8Epilogue ep) {
     constexpr int BM = T::BM, BN = T::BN, NB = T::NB, FM = T::FM, FN = T::FN, P = kPieces;
+    // An array for each stage buffer: the compiler then knows that a load into one
+    // of them does not delay reads of another.
     __shared__ uint4 b0[T::kStage], b1[T::kStage], b2[NB > 2 ? T::kStage : 1],
-        b3[NB > 3 ? T::kStage : 1];
+        b3[NB > 3 ? T::kStage : 1], b4[NB > 4 ? T::kStage : 1], b5[NB > 5 ? T::kStage : 1],
+        b6[NB > 6 ? T::kStage : 1], b7[NB > 7 ? T::kStage : 1];
+    auto buffer = [&](auto i) -> uint4* {
+        constexpr int I = decltype(i)::value % NB;
+        if constexpr (I == 0) return b0;
+        if constexpr (I == 1) return b1;
+        if constexpr (I == 2) return b2;
+        if constexpr (I == 3) return b3;
+        if constexpr (I == 4) return b4;
+        if constexpr (I == 5) return b5;
+        if constexpr (I == 6) return b6;
+        if constexpr (I == 7) return b7;
+    };
     __shared__ float sx[BM], sw[BN];
     __shared__ uint32_t touched[T::W][kWave];  // where the touching loads land; never read
     // Workgroups reach the 8 XCDs in turn: each XCD takes a run of consecutive
@@ -332,9 +425,11 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
     // the touching loads of a stage are behind its refill and may be out yet.)
     constexpr int kLoads = T::LX + T::LW, kOut = (NB - 2) * kLoads + kTouches;
     const int n = max(1, (kend - kbeg + kStageK - 1) / kStageK);
-    auto stage = [&](const uint4* b, uint4* refill, int s) {
+    auto stage = [&](auto i, int s) {  // s % NB == i
+        constexpr int I = decltype(i)::value;
+        const uint4* b = buffer(i);
         wait_and_barrier<kOut>();
-        issue(refill, (s + NB - 1) * kStageK);
+        issue(buffer(std::integral_constant<int, I + NB - 1>{}), (s + NB - 1) * kStageK);
         touch(s);
         read(b, c0, c0);
         multiply(c1);
@@ -343,31 +438,27 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
         multiply(c0);
         interleave<0, FM, FN, 0>();
     };
-    issue(b0, 0);
-    touch(-1);
-    if constexpr (NB > 2) issue(b1, kStageK);
-    if constexpr (NB > 3) issue(b2, 2 * kStageK);
     // stage 0: no products before it
+    unrolled<0, NB - 1>([&](auto i) {
+        issue(buffer(i), decltype(i)::value * kStageK);
+        if constexpr (decltype(i)::value == 0) touch(-1);
+    });
     wait_and_barrier<kOut>();
-    issue(NB == 2 ? b1 : NB == 3 ? b2 : b3, (NB - 1) * kStageK);
+    issue(buffer(std::integral_constant<int, NB - 1>{}), (NB - 1) * kStageK);
     touch(0);
     read(b0, c0, c0);
     read(b0, c1, c1);
     multiply(c0);
     int s = 1;
-    for (; s + NB <= n; s += NB) {
-        stage(b1, b0, s);
-        if constexpr (NB == 2) stage(b0, b1, s + 1);
-        if constexpr (NB > 2) stage(b2, b1, s + 1);
-        if constexpr (NB == 3) stage(b0, b2, s + 2);
-        if constexpr (NB > 3) stage(b3, b2, s + 2);
-        if constexpr (NB > 3) stage(b0, b3, s + 3);
-    }
-    if (s < n) stage(b1, b0, s);
-    if constexpr (NB > 2)
-        if (s + 1 < n) stage(b2, b1, s + 1);
-    if constexpr (NB > 3)
-        if (s + 2 < n) stage(b3, b2, s + 2);
+    for (; s + NB <= n; s += NB)
+        unrolled<1, NB + 1>([&](auto i) {
+            constexpr int I = decltype(i)::value;
+            stage(std::integral_constant<int, I % NB>{}, s + I - 1);
+        });
+    unrolled<1, NB>([&](auto i) {
+        constexpr int I = decltype(i)::value;
+        if (s + I - 1 < n) stage(i, s + I - 1);
+    });
     multiply(c1);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may outlive the workgroup's LDS
 
@@ -471,11 +562,25 @@ void launch_split(int M, int N, int K, int S, int kc, int group, const int8_t* x
                        dim3(kBlock), 0, stream, partial, M, N, tiles, group, S, ep);
 }
 
-template <int S, int RT, int MT>
+template <int S, int RT, int MT, int D>
 void launch_team(int M, int N, int K, const int8_t* xq, const int8_t* wq, const Int8Epilogue& ep,
                  hipStream_t stream) {
-    hipLaunchKernelGGL((int8_team_kernel<S, RT, MT>), dim3((N + 16 * RT - 1) / (16 * RT)),
+    hipLaunchKernelGGL((int8_team_kernel<S, RT, MT, D>), dim3((N + 16 * RT - 1) / (16 * RT)),
                        dim3(S * kWave), 0, stream, xq, wq, M, N, K, ep);
+}
+
+// The team kernel for MT 16-row tiles of x, in the forms whose slots fit in LDS.
+template <int MT>
+void launch_team(int waves, int rt, int slots, int M, int N, int K, const int8_t* xq,
+                 const int8_t* wq, const Int8Epilogue& ep, hipStream_t stream) {
+    if constexpr (MT <= 3)
+        if (rt == 2) return launch_team<8, 2, MT, 2>(M, N, K, xq, wq, ep, stream);
+    if constexpr (MT == 1)
+        if (slots == 4) return launch_team<8, 1, 1, 4>(M, N, K, xq, wq, ep, stream);
+    if (waves == 4)
+        launch_team<4, 1, MT, 2>(M, N, K, xq, wq, ep, stream);
+    else
+        launch_team<8, 1, MT, 2>(M, N, K, xq, wq, ep, stream);
 }
 
 // ---------------------------------------------------------------- choice
@@ -518,35 +623,41 @@ constexpr int kTeamMaxM = 64;
 constexpr double kStreamBytesPerUs = 5.6e6;  // W from HBM through the tile kernel
 
 struct Int8Plan {
-    bool team;
-    int waves, rt;     // team kernel: waves a workgroup, 16-row tiles of W
-    int tile, S, kc;   // tile kernel: variant, K splits, codes a split
+    enum Kind { kTeam, kWide, kTile } kind;
+    int waves, rt, slots;  // team kernel
+    int tile, S, kc;       // tile kernel: variant, K splits, codes a split
     size_t workspace;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The variant with the least estimated time (us).  Team: 2 us, then 0.038 us
-// per KB of W and 0.018 per KB of x that a compute unit takes in.  Tiles: 3 us,
-// then rounds of workgroups at the measured cost per code; a split adds the
-// reduction's launch and its traffic.
+// per KB of W and 0.012 (0.016 past 48 rows) per KB of x that a compute unit
+// takes in.  Tiles: 3 us, then rounds of workgroups at the measured cost per
+// code, but no faster than W comes from HBM; a split adds the reduction's
+// launch and its traffic.  Over 38 shapes of 1 to 4096 rows the choice was
+// within 3 % of the fastest variant on average.
 Int8Plan int8_plan(int M, int N, int K, bool tiles_only = false, bool one_split = false) {
     Int8Plan best{};
     double least = 1e30;
     if (!tiles_only && M <= kTeamMaxM) {
-        for (int rt = 1; rt <= 2; ++rt) {
+        for (int rt = 1; rt <= (M <= 48 ? 2 : 1); ++rt) {
             const double wgs = (double)ceil_div(N, 16 * rt);
             const double per = wgs > kCus ? wgs / kCus : 1.0;
-            // two row tiles a workgroup read x half as often, but measured 6 % slower on the same bytes
-            const double est = (2.0 + per * K * (0.038 * 16 * rt + 0.018 * M) / 1000.0) * (rt == 2 ? 1.06 : 1.0);
+            const double x = M <= 48 ? 0.012 : 0.016;
+            double est = 2.0 + per * K * (0.038 * 16 * rt + x * M) / 1000.0;
+            if (rt == 2 && wgs < kCus) est *= 1.04;  // idle compute units
             if (est < least) {
                 least = est;
-                // 8 waves keep more of W in flight where a workgroup has a compute unit to
-                // itself and at least two windows for every wave
-                const int waves = K <= 2048 || rt == 2 || wgs >= 1.5 * kCus ? 4 : 8;
-                best = Int8Plan{true, waves, rt, 0, 1, K, 0};
+                // 4 slots where a workgroup has a compute unit to itself; 4 waves where
+                // 8 would have one window each
+                best = Int8Plan{Int8Plan::kTeam, K <= 1024 ? 4 : 8, rt,
+                                rt == 1 && M <= 16 && wgs <= kCus && K >= 4096 ? 4 : 2, 0, 1, K, 0};
             }
         }
+        const int64_t wgs = ceil_div(N, 16);
+        if (M <= 8 && (wgs > 4 * kCus || (wgs > 1.5 * kCus && K <= 4096)))
+            best.kind = Int8Plan::kWide;
     }
     for (int v = 0; v < kTileVariants; ++v) {
         const TileCost& c = kTiles[v];
@@ -564,7 +675,7 @@ Int8Plan int8_plan(int M, int N, int K, bool tiles_only = false, bool one_split 
             if (S > 1) est += 3.0 + 8.0 * S * M * N / 4.0e6;
             if (est < least && ws <= ((size_t)1 << 30)) {
                 least = est;
-                best = Int8Plan{false, 0, 0, v, S, kc, ws};
+                best = Int8Plan{Int8Plan::kTile, 0, 0, 0, v, S, kc, ws};
             }
         }
     }
@@ -578,20 +689,19 @@ size_t int8_workspace_bytes(int M, int N, int K) { return int8_plan(M, N, K).wor
 hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t* wq,
                             const Int8Epilogue& ep, void* ws, hipStream_t stream) {
     const Int8Plan p = int8_plan(M, N, K);
-    if (p.team) {
+    if (p.kind == Int8Plan::kWide) {
+        hipLaunchKernelGGL((int8_wide_kernel<4>), dim3((N + 15) / 16), dim3(4 * kWave), 0, stream, xq,
+                           wq, M, N, K, ep);
+    } else if (p.kind == Int8Plan::kTeam) {
         auto go = [&](auto mt) {
-            constexpr int MT = decltype(mt)::value;
-            if (p.rt == 2)
-                launch_team<4, 2, MT>(M, N, K, xq, wq, ep, stream);
-            else if (p.waves == 4)
-                launch_team<4, 1, MT>(M, N, K, xq, wq, ep, stream);
-            else
-                launch_team<8, 1, MT>(M, N, K, xq, wq, ep, stream);
+            launch_team<decltype(mt)::value>(p.waves, p.rt, p.slots, M, N, K, xq, wq, ep, stream);
         };
         if (M <= 16)
             go(std::integral_constant<int, 1>{});
         else if (M <= 32)
             go(std::integral_constant<int, 2>{});
+        else if (M <= 48)
+            go(std::integral_constant<int, 3>{});
         else
             go(std::integral_constant<int, 4>{});
     } else {
@@ -605,7 +715,7 @@ hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t*
 
 bool int8_gated_ok(int M, int F, int H) {
     const Int8Plan p = int8_plan(M, 2 * F, H);
-    return !p.team && p.S == 1;
+    return p.kind == Int8Plan::kTile && p.S == 1;
 }
 
 hipError_t launch_gated_int8(int M, int F, int H, const int8_t* xq, const int8_t* wq,
