@@ -46,7 +46,8 @@ bool mlp_layout(int32_t M, int32_t H, int32_t F, MlpLayout* L) {
     const size_t m = (size_t)M;
     L->q = take(m * H);
     L->sq = take(m * 4);
-    L->u = take(m * F * 8);
+    // the projections' outputs, or (gated in the epilogue) the gated product alone
+    L->u = take(m * F * (M > 0 && sg::int8_gated_ok(M, F, H) ? 4 : 8));
     L->p = take(m * F);
     L->sp = take(m * 4);
     const size_t a = M > 0 ? sg::int8_workspace_bytes(M, 2 * F, H) : 0;

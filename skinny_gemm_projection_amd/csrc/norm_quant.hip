@@ -115,8 +115,8 @@ __device__ __forceinline__ float store_codes(float (&t)[P][8], uint32_t amax_bit
 // THREADS threads hold one row, ROWS rows a workgroup.
 template <int THREADS, int ROWS, int P>
 __global__ __launch_bounds__(THREADS* ROWS) void rmsnorm_kernel(
-    const uint16_t* __restrict__ x, const uint16_t* __restrict__ r, const uint16_t* __restrict__ g,
-    float eps, int M, int K, uint16_t* h, uint16_t* y, int8_t* codes, float* scales) {
+    const uint16_t* x, const uint16_t* r, const uint16_t* __restrict__ g, float eps, int M, int K,
+    uint16_t* h, uint16_t* y, int8_t* codes, float* scales) {  // h, y may be x or r
     static_assert(ROWS == 1 || THREADS == kWave, "several rows a workgroup: a wave each");
     const int64_t row = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? wave_id_in_block() : 0);
     if (ROWS > 1 && row >= M) return;  // whole waves; no barrier follows for them
@@ -226,14 +226,18 @@ __global__ __launch_bounds__(THREADS* ROWS) void quant_int8_kernel(const char* _
     if (tid == 0) scales[row] = bad ? __builtin_nanf("") : m / 127.0f;
 }
 
-// The row is spread over one wave, 256 or 1024 threads, whichever is the
-// first to hold it in at most 4 (1024 threads: 8) pieces a thread.
+constexpr int kFewRows = 256;
+
+// How a row is spread: over one wave, 256 or 1024 threads, whichever is the
+// first to hold it in at most 4 (1024 threads: 8) pieces a thread.  Fewer rows
+// than compute units get 1024 threads, so that one load a thread brings the row.
 template <class F>
-void with_shape(int n8, F f) {
+void with_shape(int M, int n8, F f) {
 #define SG_SHAPE(T, R, P)                                            \
     f(std::integral_constant<int, T>{}, std::integral_constant<int, R>{}, \
       std::integral_constant<int, P>{})
-    if (n8 <= 64) SG_SHAPE(64, 4, 1);
+    if (M < kFewRows && n8 > 256 && n8 <= 1024) SG_SHAPE(1024, 1, 1);
+    else if (n8 <= 64) SG_SHAPE(64, 4, 1);
     else if (n8 <= 128) SG_SHAPE(64, 4, 2);
     else if (n8 <= 256) SG_SHAPE(256, 1, 1);
     else if (n8 <= 512) SG_SHAPE(256, 1, 2);
@@ -249,7 +253,7 @@ void with_shape(int n8, F f) {
 hipError_t launch_rmsnorm(int M, int K, const uint16_t* x, const uint16_t* r, const uint16_t* g,
                           float eps, uint16_t* h, uint16_t* y, int8_t* codes, float* scales,
                           hipStream_t stream) {
-    with_shape(K / 8, [&](auto t, auto rows, auto p) {
+    with_shape(M, K / 8, [&](auto t, auto rows, auto p) {
         constexpr int T = decltype(t)::value, R = decltype(rows)::value, P = decltype(p)::value;
         hipLaunchKernelGGL((rmsnorm_kernel<T, R, P>), dim3((M + R - 1) / R), dim3(T * R), 0, stream,
                            x, r, g, eps, M, K, h, y, codes, scales);
@@ -259,7 +263,7 @@ hipError_t launch_rmsnorm(int M, int K, const uint16_t* x, const uint16_t* r, co
 
 hipError_t launch_quant_int8(int M, int K, const void* x, bool f32, bool gated, int8_t* codes,
                              float* scales, hipStream_t stream) {
-    with_shape(K / 8, [&](auto t, auto rows, auto p) {
+    with_shape(M, K / 8, [&](auto t, auto rows, auto p) {
         constexpr int T = decltype(t)::value, R = decltype(rows)::value, P = decltype(p)::value;
         const dim3 grid((M + R - 1) / R), block(T * R);
         const char* xb = static_cast<const char*>(x);

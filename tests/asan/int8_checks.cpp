@@ -48,7 +48,7 @@ void sizes() {
     for (int32_t M : Ms)
         for (int32_t H : {16, 272, 7168, SG_ROW_MAX_K})
             for (int32_t F : {16, 528, 18432, SG_ROW_MAX_K})
-                EXPECT(skinny_mlp_int8_step_workspace(M, H, F) >= (size_t)M * (H + 9 * (size_t)F));
+                EXPECT(skinny_mlp_int8_step_workspace(M, H, F) >= (size_t)M * (H + 5 * (size_t)F));
 }
 
 void refusals() {
