@@ -356,10 +356,6 @@ def _arg(t, dtype, shape, name, dev):
     raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _opt(t, dtype, shape, name, dev):
-    return None if t is None else _arg(t, dtype, shape, name, dev)
-
-
 def _rows(x, name, dtypes):
     """(rows, columns, device, pointer) of a contiguous 2-D device tensor of one of the types."""
     if not isinstance(x, torch.Tensor):
@@ -396,15 +392,19 @@ def _ws_arg(workspace, nbytes, dev, stream):
     return workspace, _ptr(workspace, torch.uint8, "workspace", dev), workspace.numel()
 
 
-# The raw handle of a device's current stream; torch.cuda.current_stream makes a Stream object
-# first, which costs more host time than the rest of a call's argument checks.
-_current_stream = torch._C._cuda_getCurrentRawStream if torch.version.hip else None
+def _raw_current():
+    """The functions behind torch.cuda.current_stream and current_device, without the Stream
+    object and the initialisation check that cost more host time than all checks of a call
+    (its tensors are on the device already, so the runtime is up)."""
+    return torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _run_on(dev, stream, fn, *args):
     """fn(*args, stream handle) with dev current; the default stream is dev's current one."""
-    handle = _current_stream(dev.index) if stream is None else _stream(stream)
-    if dev.index == torch.cuda.current_device():
+    raw_stream, raw_device = _raw_current()
+    index = dev.index
+    handle = raw_stream(index) if stream is None else _stream(stream)
+    if raw_device() == index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -427,11 +427,12 @@ def skinny_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, r=None, h=None,
         codes = _new((M, K), torch.int8, dev, stream)
     if codes is not None and scales is None:
         scales = _new((M,), torch.float32, dev, stream)
-    _run_on(dev, stream, _c().skinny_rmsnorm, M, K, px, _opt(r, bf16, mk, "r", dev),
-            _arg(g, bf16, (K,), "g", dev), eps,
-            _opt(h, bf16, mk, "h", dev), _opt(y_bf16, bf16, mk, "y_bf16", dev),
-            _opt(codes, torch.int8, mk, "codes", dev),
-            _opt(scales, torch.float32, (M,), "scales", dev))
+    _run_on(dev, stream, _c().skinny_rmsnorm, M, K, px,
+            None if r is None else _arg(r, bf16, mk, "r", dev), _arg(g, bf16, (K,), "g", dev), eps,
+            None if h is None else _arg(h, bf16, mk, "h", dev),
+            None if y_bf16 is None else _arg(y_bf16, bf16, mk, "y_bf16", dev),
+            None if codes is None else _arg(codes, torch.int8, mk, "codes", dev),
+            None if scales is None else _arg(scales, torch.float32, (M,), "scales", dev))
     return h, y_bf16, codes, scales
 
 
@@ -505,7 +506,8 @@ def skinny_mlp_int8_step(x: torch.Tensor, g: torch.Tensor, eps: float, W_gate_up
                                    stream)
     i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
     step = SgMlpInt8Step(
-        px, _opt(r, bf16, (M, H), "r", dev), _arg(g, bf16, (H,), "g", dev), _arg(W_gate_up, i8, (2 * F, H), "W_gate_up", dev),
+        px, None if r is None else _arg(r, bf16, (M, H), "r", dev),
+        _arg(g, bf16, (H,), "g", dev), _arg(W_gate_up, i8, (2 * F, H), "W_gate_up", dev),
         _arg(gate_up_scales, f32, (2 * F,), "gate_up_scales", dev),
         _arg(W_down, i8, (H, F), "W_down", dev), _arg(down_scales, f32, (H,), "down_scales", dev),
         _arg(out, bf16, (M, H), "out", dev), M, H, F, eps)

@@ -423,3 +423,167 @@ def test_weights_quantised_by_the_row_quantiser():
     hx, hw = 0.5 * xs.cpu().double()[:, None], 0.5 * ws.cpu().double()[None, :]
     ax, aw = x.double().abs().sum(dim=1)[:, None], W.double().abs().sum(dim=1)[None, :]
     assert ((y.cpu().double() - want).abs() <= (hx * aw + hw * ax + K * hx * hw) * 1.001).all()
+
+
+# ------------------------------------------------------------------ calls the documentation allows
+
+
+def product_inputs(M, N, K, seed):
+    cpu = rand_codes(M, K, seed), rand_scales(M, seed + 1), rand_codes(N, K, seed + 2), rand_scales(N, seed + 3)
+    return cpu, [t.to(DEV) for t in cpu]
+
+
+SPLIT = [(61, 512, 8192), (100, 257, 16384), (40, 4096, 7168)]
+
+
+@pytest.mark.parametrize("M,N,K", SPLIT)
+def test_gemm_split_between_workgroups(M, N, K):
+    """A K that is split goes through the caller's workspace, whatever that held before; a
+    workspace longer than needed is left alone behind its end."""
+    announce(f"int8 split M={M} N={N} K={K}")
+    need = sg.skinny_gemm_int8_workspace(M, N, K)
+    cpu, d = product_inputs(M, N, K, 5)
+    want = ref.linear(*cpu)
+    for fill in (0, 255):
+        ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device=DEV)
+        y, _ = sg.skinny_gemm_int8(*d, workspace=ws)
+        same(y, want, f"workspace of {fill}")
+        assert (ws[need:] == fill).all()
+    if need:
+        before = sg.skinny_gemm_get_counters()
+        with pytest.raises(sg.SkinnyGemmError) as e:
+            sg.skinny_gemm_int8(*d, workspace=torch.empty(need - 16, dtype=torch.uint8, device=DEV))
+        assert e.value.status == 5
+        assert counters_delta(before, sg.skinny_gemm_get_counters()) == [0] * sg.SG_NUM_COUNTERS
+
+
+def test_two_captured_graphs_and_eager_calls():
+    """Two graphs, each with a workspace of its own, replayed in turn with eager calls between."""
+    sets = []
+    for seed, (M, N, K) in ((5, SPLIT[0]), (50, SPLIT[1])):
+        cpu, d = product_inputs(M, N, K, seed)
+        ws = torch.empty(max(16, sg.skinny_gemm_int8_workspace(M, N, K)), dtype=torch.uint8, device=DEV)
+        y = torch.empty((M, N), device=DEV)
+        sg.skinny_gemm_int8(*d, y_f32=y, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sg.skinny_gemm_int8(*d, y_f32=y, workspace=ws)
+        sets.append((g, d, y, cpu))
+    for i in range(4):
+        for g, d, y, cpu in sets:
+            d[1].copy_(rand_scales(d[1].shape[0], 900 + i))
+            y.zero_()
+            g.replay()
+            eager, _ = sg.skinny_gemm_int8(*d)
+            same(y, eager, f"replay {i}")
+            same(y, ref.linear(cpu[0], d[1].cpu(), cpu[2], cpu[3]), f"replay {i}")
+
+
+def test_streams_given_and_current():
+    """Work goes to the stream given (a Stream or a handle), else to the current one."""
+    cpu, d = product_inputs(33, 300, 2064, 8)
+    want = ref.linear(*cpu)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y, _ = sg.skinny_gemm_int8(*d, stream=s)
+    s.synchronize()
+    same(y, want, "stream given")
+    y, _ = sg.skinny_gemm_int8(*d, stream=s.cuda_stream)
+    s.synchronize()
+    same(y, want, "handle given")
+    with torch.cuda.stream(s):
+        y, _ = sg.skinny_gemm_int8(*d)
+    s.synchronize()
+    same(y, want, "current stream")
+    x = normal((5, 1032), 1)
+    with torch.cuda.stream(s):
+        c, sc = sg.skinny_quant_int8(x.to(DEV))
+    s.synchronize()
+    check_quant(x, False, c, sc, "current stream")
+
+
+def test_refusals_before_anything_runs():
+    q, qs = torch.zeros((3, 64), dtype=torch.int8, device=DEV), torch.ones(3, device=DEV)
+    w, ws = torch.zeros((5, 64), dtype=torch.int8, device=DEV), torch.ones(5, device=DEV)
+    x = torch.zeros((3, 64), dtype=BF16, device=DEV)
+    g = torch.ones(64, dtype=BF16, device=DEV)
+    y, y16 = torch.empty((3, 5), device=DEV), torch.empty((3, 5), device=DEV, dtype=BF16)
+    before = sg.skinny_gemm_get_counters()
+
+    def refused(kind, f, *a, **kw):
+        with pytest.raises(kind):
+            f(*a, **kw)
+
+    f = sg.skinny_gemm_int8
+    refused(ValueError, f, q, qs[:2], w, ws)
+    refused(ValueError, f, q, qs, w, ws[:4])
+    refused(ValueError, f, q, qs, w[:, :48], ws)
+    refused(ValueError, f, q[:, :48], qs, w[:, :48].contiguous(), ws)  # not contiguous
+    refused(ValueError, f, q, qs, w.cpu(), ws)
+    refused(ValueError, f, q, qs, w, ws, y_f32=y.t())
+    refused(TypeError, f, q, qs, w, ws, y_f32=y16)
+    refused(TypeError, f, q, qs.double(), w, ws)
+    refused(TypeError, f, q, qs, w.to(torch.uint8), ws)
+    refused(ValueError, f, q, qs, w, ws, r=y16[:2])
+    refused(sg.SkinnyGemmError, f, q[:, :24].contiguous(), qs, w[:, :24].contiguous(), ws)
+    refused(TypeError, f, q, qs, w, ws, workspace=qs)
+    n = sg.skinny_rmsnorm
+    refused(ValueError, n, x, g[:32], 1e-6)
+    refused(ValueError, n, x, g, 1e-6, r=x[:2])
+    refused(TypeError, n, x, g.float(), 1e-6)
+    refused(sg.SkinnyGemmError, n, x, g, 0.0)
+    refused(ValueError, n, x, g, 1e-6, codes=q[:2])
+    refused(sg.SkinnyGemmError, sg.skinny_quant_int8, x[:, :12].contiguous())
+    refused(ValueError, sg.skinny_quant_int8, x, gated=True, codes=q)
+    wgu, wd = torch.zeros((64, 64), dtype=torch.int8, device=DEV), torch.zeros((64, 32), dtype=torch.int8, device=DEV)
+    one = torch.ones(64, device=DEV)
+    refused(ValueError, sg.skinny_mlp_int8_step, x, g, 1e-6, wgu[:48], one, wd, one)
+    refused(sg.SkinnyGemmError, sg.skinny_mlp_int8_step, x, g, float("nan"), wgu, one, wd, one)
+    refused(ValueError, sg.skinny_mlp_int8_step, x, g, 1e-6, wgu, one, wd, one, out=x.t())
+    assert counters_delta(before, sg.skinny_gemm_get_counters()) == [0] * sg.SG_NUM_COUNTERS
+
+
+def test_offsets_past_32_bits():
+    """Outputs, activations and weights past 4 GB; sampled rows against the references."""
+    f = dict(device=DEV)
+    announce("int8 output past 2^31 elements")
+    M, N, K = 65700, 32784, 32
+    xq, wq = [torch.randint(-128, 128, s, dtype=torch.int8, **f) for s in ((M, K), (N, K))]
+    xs, ws = torch.rand(M, **f) + 0.5, torch.rand(N, **f) + 0.5
+    y = torch.empty((M, N), dtype=BF16, **f)
+    sg.skinny_gemm_int8(xq, xs, wq, ws, y_bf16=y)
+    at = torch.tensor([0, 1, 255, 256, 32767, 65533, 65535, 65536, M - 1])
+    same(y[at.to(DEV)], ref.linear(xq.cpu()[at], xs.cpu()[at], wq.cpu(), ws.cpu()).to(BF16), "rows")
+    del y
+    announce("int8 weights and codes past 2^32 bytes")
+    for M, N, K in ((3, 69000, 65536), (69000, 40, 65536), (300, 69000, 65536)):
+        xq, wq = [torch.randint(-128, 128, s, dtype=torch.int8, **f) for s in ((M, K), (N, K))]
+        xs, ws = torch.rand(M, **f), torch.rand(N, **f)
+        y, _ = sg.skinny_gemm_int8(xq, xs, wq, ws)
+        r, c = torch.tensor([0, M // 2, M - 1]), torch.tensor([0, N // 2, N - 2, N - 1])
+        want = ref.linear(xq[r.to(DEV)].cpu(), xs.cpu()[r], wq[c.to(DEV)].cpu(), ws.cpu()[c])
+        same(y.cpu()[r][:, c], want, f"M={M} N={N}")
+    announce("rows past 2^32 bytes")
+    M, K = 70000, 32776
+    x = torch.randn((M, K), dtype=BF16, **f)
+    g = torch.ones(K, dtype=BF16, **f)
+    _, _, codes, scales = sg.skinny_rmsnorm(x, g, EPS)
+    r = torch.tensor([0, 65535, 65536, M - 1], device=DEV)
+    check_norm(x[r].cpu(), None, g.cpu(), EPS, None, None, codes[r], scales[r], "norm")
+    codes, scales = sg.skinny_quant_int8(x, codes=codes, scales=scales)
+    check_quant(x[r].cpu(), False, codes[r], scales[r], "codes")
+
+
+@pytest.mark.parametrize("M,H,F", [(2, 65536, 48), (2, 48, 65536), (260, 65536, 8208), (5, 64, 32)])
+def test_mlp_widest_rows(M, H, F):
+    announce(f"mlp widest M={M} H={H} F={F}")
+    f = dict(device=DEV)
+    x, r = normal((M, H), 1).to(DEV), normal((M, H), 2).to(DEV)
+    g = torch.ones(H, dtype=BF16, **f)
+    wgu = torch.randint(-127, 128, (2 * F, H), dtype=torch.int8, **f)
+    wd = torch.randint(-127, 128, (H, F), dtype=torch.int8, **f)
+    sgu, sd = torch.rand(2 * F, **f) * 1e-3 / H ** 0.5, torch.rand(H, **f) * 1e-3 / F ** 0.5
+    out = sg.skinny_mlp_int8_step(x, g, EPS, wgu, sgu, wd, sd, r=r)
+    same(out, parts(x, r, g, wgu, sgu, wd, sd)[-1], "step")
+    assert torch.isfinite(out.float()).all()
