@@ -51,7 +51,14 @@ GEMM = [(1, 1, 16), (1, 40, 16), (1, 129, 112), (1, 1024, 1024), (1, 200, 8208),
         (65, 130, 192), (96, 500, 1008), (100, 1000, 4096), (128, 128, 128), (129, 255, 160),
         (200, 37, 9008), (255, 257, 640), (256, 256, 2048), (257, 513, 144), (300, 1001, 2064),
         (511, 1030, 528), (513, 5, 272), (700, 777, 1040), (1025, 1281, 256), (2049, 300, 528),
-        (1000, 2051, 2064)]
+        (1000, 2051, 2064),
+        # wide W: two row tiles a workgroup, x in registers, every tile size (the last two
+        # sizes' rows unaligned and aligned), K split with each
+        (9, 8195, 1040), (1, 8196, 4112), (17, 8195, 1040), (33, 7170, 1040), (33, 8200, 1296),
+        (9, 8195, 16), (1, 6147, 1040), (8, 20003, 528), (5, 6148, 2064), (400, 16390, 144),
+        (513, 16392, 272), (129, 16390, 272), (140, 16384, 528), (65, 16390, 400), (70, 16400, 144),
+        (65, 8195, 400), (77, 8192, 272), (129, 6147, 8208), (129, 16390, 6160), (129, 16388, 6160),
+        (4097, 17, 3088), (3000, 64, 4112)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)
@@ -327,7 +334,9 @@ def parts(x, r, g, wgu, sgu, wd, sd):
 
 
 MLP = [(1, 512, 1024), (1, 16, 16), (2, 7168, 2064), (4, 1040, 2064), (16, 528, 272), (33, 272, 1040),
-       (61, 1024, 4112), (65, 528, 1040), (130, 1040, 784), (300, 512, 1296), (1025, 272, 528)]
+       (61, 1024, 4112), (65, 528, 1040), (130, 1040, 784), (300, 512, 1296), (1025, 272, 528),
+       # every tile size with the gated product in its epilogue
+       (65, 272, 8208), (129, 144, 8208), (257, 144, 12304), (400, 272, 8208)]
 
 
 @pytest.mark.parametrize("M,H,F", MLP)
