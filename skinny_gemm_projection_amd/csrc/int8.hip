@@ -125,6 +125,21 @@ __device__ __forceinline__ float4 channel_scales(const float* ws, int N, int n) 
 
 // ---------------------------------------------------------------- team kernels
 
+// Where a workgroup of the team kernels starts in K.  Rows whose pitch is a
+// multiple of 4 KB have the same window in the same memory channels, and
+// workgroups that all start at window 0 queue there together: such rows are
+// started 7 windows apart and wrap around.  (16 x 7168 x 8192 takes 11.4 us
+// against 14.1 without; other pitches lose about 1 %, so they start at 0.)
+__device__ __forceinline__ int first_window(int K, int windows) {
+    return K % 4096 == 0 ? (int)(blockIdx.x * 7u % (uint32_t)windows) : 0;
+}
+
+// Window of a slot: the slots behind the last are empty (past K).
+__device__ __forceinline__ int window_of(int slot, int first, int windows) {
+    const int t = slot + first;
+    return slot >= windows ? windows : t >= windows ? t - windows : t;
+}
+
 // Sums of the S waves of a workgroup (RT * MT blocks of 16 x 16 each, in the
 // LDS at sums + wave * stride) and the finished outputs.
 template <int S, int RT, int MT>
@@ -173,8 +188,10 @@ __global__ __launch_bounds__(S* kWave) void int8_team_kernel(const int8_t* __res
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
     const int lrow = lane / P, kpos = ((lane % P) ^ lrow) * 16;
+    const int rounds = max(1, (K + kWin * S - 1) / (kWin * S));  // every load issued is used
+    const int windows = rounds * S, first = first_window(K, windows);
     auto load = [&](int round, uint4* slot) {
-        const int k = (round * S + wave) * kWin + kpos;
+        const int k = window_of(round * S + wave, first, windows) * kWin + kpos;
         const uint32_t at = k < K ? (uint32_t)lrow * K + k : kPastEnd;
 #pragma unroll
         for (int i = 0; i < 16 * RT / kRows; ++i)
@@ -198,7 +215,6 @@ __global__ __launch_bounds__(S* kWave) void int8_team_kernel(const int8_t* __res
             }
         }
     };
-    const int rounds = max(1, (K + kWin * S - 1) / (kWin * S));  // every load issued is used
     load(0, slot0[wave]);
     load(1, slot1[wave]);
     if constexpr (D > 2) load(2, slot2[wave]), load(3, slot3[wave]);
@@ -243,8 +259,10 @@ __global__ __launch_bounds__(S* kWave) void int8_wide_kernel(const int8_t* __res
 
     i32x4_t acc = {0, 0, 0, 0};
     uint4 x0[4], x1[4];
+    const int rounds = max(1, (K + kWin * S - 1) / (kWin * S));  // every load issued is used
+    const int windows = rounds * S, first = first_window(K, windows);
     auto load = [&](int round, uint4* slot, uint4 (&x)[4]) {
-        const int k = (round * S + wave) * kWin;
+        const int k = window_of(round * S + wave, first, windows) * kWin;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 4 rows x 256 bytes, piece p of row r at place p ^ r
             const int r = 4 * i + grp, kk = k + ((row ^ r) * 16);
@@ -260,7 +278,6 @@ __global__ __launch_bounds__(S* kWave) void int8_wide_kernel(const int8_t* __res
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc = mfma16(slot[row * 16 + ((t * 4 + grp) ^ row)], x[t], acc);
     };
-    const int rounds = max(1, (K + kWin * S - 1) / (kWin * S));  // every load issued is used
     load(0, slot0[wave], x0);
     load(1, slot1[wave], x1);
     for (int r = 0; r < rounds; r += 2) {
@@ -697,7 +714,9 @@ Int8Plan int8_plan(int M, int N, int K, bool tiles_only = false, bool one_split 
             const double per = wgs > kCus ? wgs / kCus : 1.0;
             const double x = M <= 48 ? 0.012 : 0.016;
             double est = 2.0 + per * K * (0.038 * 16 * rt + x * M) / 1000.0;
-            if (rt == 2 && wgs < kCus) est *= 1.04;  // idle compute units
+            // two row tiles: idle compute units where they do not fill the GPU; at pitches
+            // of a multiple of 4 KB faster (16 x 8192 x 8192 12.2 us, one tile 13.9)
+            if (rt == 2) est *= K % 4096 == 0 ? 0.88 : wgs < kCus ? 1.04 : 1.0;
             if (est < least) {
                 least = est;
                 // 4 slots where a workgroup has a compute unit to itself; 4 waves where

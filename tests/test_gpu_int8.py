@@ -58,7 +58,10 @@ GEMM = [(1, 1, 16), (1, 40, 16), (1, 129, 112), (1, 1024, 1024), (1, 200, 8208),
         (9, 8195, 16), (1, 6147, 1040), (8, 20003, 528), (5, 6148, 2064), (400, 16390, 144),
         (513, 16392, 272), (129, 16390, 272), (140, 16384, 528), (65, 16390, 400), (70, 16400, 144),
         (65, 8195, 400), (77, 8192, 272), (129, 6147, 8208), (129, 16390, 6160), (129, 16388, 6160),
-        (4097, 17, 3088), (3000, 64, 4112)]
+        (4097, 17, 3088), (3000, 64, 4112),
+        # row pitches of a multiple of 4 KB: every workgroup starts elsewhere in K
+        (1, 300, 4096), (16, 1000, 8192), (3, 8200, 4096), (20, 8195, 4096), (5, 20001, 4096),
+        (40, 500, 12288), (50, 100, 4096), (2, 17, 16384)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)
