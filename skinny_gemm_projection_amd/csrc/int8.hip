@@ -9,18 +9,22 @@
 // four neighbours of one row of y.  The int32 sums are exact, so no split of K
 // changes a bit.
 //
-// Two kernels share the batch range:
-//  * int8_team_kernel (small batches): a workgroup owns 16 * RT rows of W and
-//    all of K, its waves take 256-code windows in turn and add their sums in
-//    LDS.  What bounds it is the weight stream from HBM, then the x rows every
-//    workgroup reads from L2.
-//  * int8_tile_kernel (larger ones): a workgroup owns BM rows of x and BN rows
-//    of W, both brought to LDS by its own loads a few stages ahead; K may be
-//    split between workgroups, the int32 partial tiles then go through the
-//    workspace to int8_reduce_kernel.  Bound by the matrix cores at long
-//    prompts.
-// Both bring W to LDS with loads that write LDS directly and whole 128-byte
-// lines per instruction where the weight stream is what counts.
+// Two kinds of kernel share the batch range:
+//  * team kernels (up to 64 rows): a workgroup owns 16 or 32 rows of W and all
+//    of K, its waves take windows of K in turn and add their sums in LDS.  Bound
+//    by the weight stream from HBM and, from about 16 rows, by the x rows that
+//    every workgroup reads from L2.  2 x 8192 x 7168 takes 10.9 us (5.4 TB/s; a
+//    kernel that only reads W 9.5), 16 x 8192 x 7168 11.1, 4 x 36864 x 7168 40.5
+//    (6.5 TB/s).
+//  * int8_tile_kernel (beyond): a workgroup owns BM rows of x and BN rows of W,
+//    both requested a few stages ahead; K may be split between workgroups, the
+//    int32 partial tiles then go through the workspace to int8_reduce_kernel.
+//    8192 x 8192 x 7168 takes 336 us (2.87 POP/s) on inputs that stay in the
+//    caches and 360 on changing ones; all-zero codes take 271, so the rest is
+//    the clock that the chip's power allows: the matrix cores are busy 70 % of
+//    the cycles at about 1.8 GHz.
+// All of them bring codes to LDS with loads that write it directly, 128-byte
+// lines whole.
 #include <type_traits>
 
 #include "int8_device.h"
@@ -330,14 +334,15 @@ constexpr int kPieces = kStageK / 16;     // 16-byte pieces of a row
 constexpr int kRowsPerLoad = 1024 / kStageK;  // a load instruction is 1 KB
 
 // Geometry of a tile variant: WM x WN waves, each FM 16-row tiles of x times FN
-// of W; NB stage buffers.
+// of W; NB stage buffers.  (More buffers for the small tiles, up to 8, changed
+// nothing: 61 x 4096 x 7168 11.6 to 12.0 us.)
 template <int WM_, int WN_, int FM_, int FN_, int NB_>
 struct TileShape {
     static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, NB = NB_;
     static constexpr int W = WM * WN, BM = WM * FM * 16, BN = WN * FN * 16;
     static constexpr int LX = BM / kRowsPerLoad / W, LW = BN / kRowsPerLoad / W;
     static_assert(LX * kRowsPerLoad * W == BM && LW * kRowsPerLoad * W == BN, "whole loads a wave");
-    static_assert(NB >= 2 && NB <= 8, "two to eight stage buffers");
+    static_assert(NB >= 2 && NB <= 4, "two to four stage buffers");
     static constexpr int kStage = (BM + BN) * kPieces;  // 16-byte pieces
 };
 
@@ -349,18 +354,13 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
     // An array for each stage buffer: the compiler then knows that a load into one
     // of them does not delay reads of another.
     __shared__ uint4 b0[T::kStage], b1[T::kStage], b2[NB > 2 ? T::kStage : 1],
-        b3[NB > 3 ? T::kStage : 1], b4[NB > 4 ? T::kStage : 1], b5[NB > 5 ? T::kStage : 1],
-        b6[NB > 6 ? T::kStage : 1], b7[NB > 7 ? T::kStage : 1];
+        b3[NB > 3 ? T::kStage : 1];
     auto buffer = [&](auto i) -> uint4* {
         constexpr int I = decltype(i)::value % NB;
         if constexpr (I == 0) return b0;
         if constexpr (I == 1) return b1;
         if constexpr (I == 2) return b2;
         if constexpr (I == 3) return b3;
-        if constexpr (I == 4) return b4;
-        if constexpr (I == 5) return b5;
-        if constexpr (I == 6) return b6;
-        if constexpr (I == 7) return b7;
     };
     __shared__ float sx[BM], sw[BN];
     __shared__ uint32_t touched[T::W][kWave];  // where the touching loads land; never read
@@ -425,15 +425,17 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
     constexpr bool kTouch = NB == 2;
     constexpr int kAhead = 4, kShareX = 8, kShareW = 4, kTouches = kTouch ? 2 : 0;
     constexpr int kLinesX = BM / kShareX / T::W, kLinesW = BN / kShareW / T::W;  // a wave's
-    const uint32_t tx = lane < kLinesX ? (uint32_t)((n0 / BC % kShareX * T::W + w) * kLinesX + lane) * K + kbeg
-                                       : kPastEnd;
-    const uint32_t tw = lane < kLinesW ? (uint32_t)((m0 / BM % kShareW * T::W + w) * kLinesW + lane) * K + kbeg
-                                       : kPastEnd;
+    const int line_x = (n0 / BC % kShareX * T::W + w) * kLinesX;
+    const int line_w = (m0 / BM % kShareW * T::W + w) * kLinesW;
+    const bool up_lines = OUT == kTileGated && line_w >= BC;
+    const uint32_t tx = lane < kLinesX ? (uint32_t)(line_x + lane) * K + kbeg : kPastEnd;
+    const uint32_t tw =
+        lane < kLinesW ? (uint32_t)(line_w - (up_lines ? BC : 0) + lane) * K + kbeg : kPastEnd;
     auto touch = [&](int stage) {
         if constexpr (kTouch) {
             const int k0 = (stage + kAhead) * kStageK;
             const bool ok = k0 < kend - kbeg;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)touched[w], 4,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(up_lines ? ru : rw, (lds_void_t*)touched[w], 4,
                                                      (int)(ok ? tw + k0 : kPastEnd), 0, 0, kCached);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)touched[w], 4,
                                                      (int)(ok ? tx + k0 : kPastEnd), 0, 0, kCached);
