@@ -80,7 +80,7 @@ typedef enum {
     SG_KERNEL_ROUTER_TOPK = 8,  /* router top-k expert selection                   */
     SG_KERNEL_MXFP4 = 9,        /* projection with block-scaled 4-bit weights      */
     SG_KERNEL_FP8 = 10,         /* projection with block-scaled 8-bit weights      */
-    SG_KERNEL_INT8 = 11,        /* product of int8 codes (main launch)             */
+    SG_KERNEL_INT8 = 11,        /* product of int8 codes (one or two launches)     */
     SG_KERNEL_RMSNORM = 12,     /* root-mean-square norm (+ residual, int8 codes)  */
     SG_KERNEL_QUANT_INT8 = 13   /* per-row int8 codes (optionally of a gated product) */
 } sg_kernel;

@@ -74,8 +74,8 @@ __device__ __forceinline__ void scale4(const i32x4_t acc, const float4 ws, float
 // Outputs y[m][n .. n+4) with the residual; rows of a multiple of 4 elements
 // keep the four together.
 __device__ __forceinline__ void finish4(const Int8Epilogue& ep, int N, int m, int n, float (&y)[4]) {
-    const int64_t at = (int64_t)m * N + n;
-    if ((N & 3) == 0) {
+    const int64_t at = (int64_t)m * ep.ld + n;
+    if ((ep.ld & 3) == 0) {
         if (ep.r) {
             const uint2 r = *reinterpret_cast<const uint2*>(ep.r + at);
             y[0] = as_f(r.x << 16) + y[0];
@@ -113,7 +113,7 @@ __device__ __forceinline__ void finish_block(const Int8Epilogue& ep, int M, int 
         const int row = r + lane / COLS, m = m0 + row;
         if (m >= M || n >= N) continue;
         float y = block[row * (COLS + 4) + col];
-        const int64_t at = (int64_t)m * N + n;
+        const int64_t at = (int64_t)m * ep.ld + n;
         if (ep.r) y = bf16_to_f32(ep.r[at]) + y;
         if (ep.y_f32) ep.y_f32[at] = y;
         if (ep.y_bf16) ep.y_bf16[at] = f32_to_bf16(y);
@@ -381,13 +381,13 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
     const rsrc_t rx = make_rsrc(xq + (int64_t)m0 * K, (uint32_t)min(BM, M - m0) * (uint32_t)K);
     const uint32_t wbytes = (uint32_t)min(BC, N - n0) * (uint32_t)K;
     const rsrc_t rw = make_rsrc(wq + (int64_t)n0 * K, wbytes);
-    const rsrc_t ru = make_rsrc(wq + ((int64_t)n0 + (OUT == kTileGated ? N : 0)) * K, wbytes);
+    const rsrc_t ru = make_rsrc(wq + ((int64_t)n0 + (OUT == kTileGated ? ep.up : 0)) * K, wbytes);
     if constexpr (OUT != kTilePartial) {
         for (int i = threadIdx.x; i < BM; i += T::W * kWave) sx[i] = m0 + i < M ? ep.xs[m0 + i] : 0.0f;
         for (int i = threadIdx.x; i < BN; i += T::W * kWave) {
             if constexpr (OUT == kTileGated) {
                 const int c = n0 + i / 32 * 16 + i % 16;
-                sw[i] = c < N ? ep.ws[c + (i % 32 >= 16 ? N : 0)] : 0.0f;
+                sw[i] = c < N ? ep.ws[c + (i % 32 >= 16 ? ep.up : 0)] : 0.0f;
             } else {
                 sw[i] = n0 + i < N ? ep.ws[n0 + i] : 0.0f;
             }
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
             for (int j = 0; j < FM; ++j)
                 if (m0 + (wm * FM + j) * 16 < M)
                     reinterpret_cast<i32x4_t*>(out)[((w * FN + i) * FM + j) * kWave + lane] = acc[i][j];
-    } else if (OUT == kTileFinal && (N & 3) != 0) {
+    } else if (OUT == kTileFinal && (ep.ld & 3) != 0) {
         constexpr int kCols = FN * 16;
         // the stage buffers are free: the last reads were before the last products
         float* block = reinterpret_cast<float*>(b0) + w * 16 * (kCols + 4);
@@ -560,7 +560,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
                     scale4(acc[i + 1][j], *reinterpret_cast<const float4*>(&sw[nl + 16]), xs, u);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) y[v] = gated_product(y[v], u[v]);
-                    *reinterpret_cast<float4*>(ep.y_f32 + (int64_t)m * N + c) =
+                    *reinterpret_cast<float4*>(ep.y_f32 + (int64_t)m * ep.ld + c) =
                         make_float4(y[0], y[1], y[2], y[3]);
                 } else {
                     if (n0 + nl >= N) continue;
@@ -697,6 +697,7 @@ struct Int8Plan {
     int waves, rt, slots;  // team kernel
     int tile, S, kc;       // tile kernel: variant, K splits, codes a split
     size_t workspace;
+    int cols, rest;        // columns of the first launch (0: all), variant of the others' tiles
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -724,33 +725,52 @@ Int8Plan int8_plan(int M, int N, int K, bool tiles_only = false, bool one_split 
                 // 4 slots where a workgroup has a compute unit to itself; 4 waves where
                 // 8 would have one window each
                 best = Int8Plan{Int8Plan::kTeam, K <= 1024 ? 4 : 8, rt,
-                                rt == 1 && M <= 16 && wgs <= kCus && K >= 4096 ? 4 : 2, 0, 1, K, 0};
+                                rt == 1 && M <= 16 && wgs <= kCus && K >= 4096 ? 4 : 2, 0, 1, K, 0, 0, 0};
             }
         }
         const int64_t wgs = ceil_div(N, 16);
         if (M <= 8 && (wgs > 4 * kCus || (wgs > 1.5 * kCus && K <= 4096)))
             best.kind = Int8Plan::kWide;
     }
+    const double stream = (double)N * K / kStreamBytesPerUs;
+    // us of rounds of tiles over n columns, kc codes each
+    auto tiles_us = [&](int v, int64_t n, int S, int kc) {
+        const TileCost& c = kTiles[v];
+        const int64_t wgs = ceil_div(M, c.bm) * ceil_div(n, c.bn) * S, slots = (int64_t)kCus * c.per_cu;
+        const int64_t rem = wgs % slots;
+        return kc * (wgs / slots * c.full + (rem == 0 ? 0.0 : rem <= kCus ? c.single : c.full)) / 1000.0;
+    };
     for (int v = 0; v < kTileVariants; ++v) {
         const TileCost& c = kTiles[v];
         const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn);
         for (int S = 1; S <= (one_split ? 1 : 16); ++S) {
             const int kc = S == 1 ? K : (int)ceil_div(ceil_div(K, S), kStageK) * kStageK;
             if (S > 1 && (kc < 4 * kStageK || (int64_t)(S - 1) * kc >= K)) break;
-            const int64_t wgs = tiles * S, slots = (int64_t)kCus * c.per_cu;
-            const int64_t rounds = wgs / slots, rem = wgs % slots;
-            const double tail = rem == 0 ? 0.0 : rem <= kCus ? c.single : c.full;
-            const double stream = (double)N * K / kStreamBytesPerUs;
-            double est = kc * (rounds * c.full + tail) / 1000.0;
+            double est = tiles_us(v, N, S, kc);
             est = 3.0 + (est > stream ? est : stream);
             const size_t ws = S > 1 ? (size_t)S * tiles * c.bm * c.bn * 4 : 0;
             if (S > 1) est += 3.0 + 8.0 * S * M * N / 4.0e6;
             if (est < least && ws <= ((size_t)1 << 30)) {
                 least = est;
-                best = Int8Plan{Int8Plan::kTile, 0, 0, 0, v, S, kc, ws};
+                best = Int8Plan{Int8Plan::kTile, 0, 0, 0, v, S, kc, ws, 0, 0};
             }
         }
     }
+    // Whole rounds of the largest tiles, then a second launch over the columns
+    // that would leave most of the GPU idle in a last round of theirs: 1000 x
+    // 36864 x 7168 227 us against 254 in one launch, 5000 x 4096 x 4096 79
+    // against 89, 1501 x 36864 x 7168 339 against 350.
+    const TileCost& big = kTiles[0];
+    const int64_t rounds = ceil_div(M, big.bm) * ceil_div(N, big.bn) / kCus;
+    const int64_t cols = rounds * kCus / ceil_div(M, big.bm) * big.bn;
+    if (rounds >= 1 && cols > 0 && cols < N)
+        for (int v = 1; v < kTileVariants; ++v) {
+            const double est = 6.0 + tiles_us(0, cols, 1, K) + tiles_us(v, N - cols, 1, K);
+            if (est < least) {
+                least = est;
+                best = Int8Plan{Int8Plan::kTile, 0, 0, 0, 0, 1, K, 0, (int)cols, v};
+            }
+        }
     return best;
 }
 
@@ -758,9 +778,21 @@ Int8Plan int8_plan(int M, int N, int K, bool tiles_only = false, bool one_split 
 
 size_t int8_workspace_bytes(int M, int N, int K) { return int8_plan(M, N, K).workspace; }
 
+// The outputs and weights from column `cols` on.
+static Int8Epilogue columns_from(const Int8Epilogue& ep, int cols) {
+    Int8Epilogue e = ep;
+    e.ws += cols;
+    if (e.y_f32) e.y_f32 += cols;
+    if (e.y_bf16) e.y_bf16 += cols;
+    if (e.r) e.r += cols;
+    return e;
+}
+
 hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t* wq,
-                            const Int8Epilogue& ep, void* ws, hipStream_t stream) {
+                            const Int8Epilogue& epilogue, void* ws, hipStream_t stream) {
     const Int8Plan p = int8_plan(M, N, K);
+    Int8Epilogue ep = epilogue;
+    ep.ld = N;
     if (p.kind == Int8Plan::kWide) {
         hipLaunchKernelGGL((int8_wide_kernel<4>), dim3((N + 15) / 16), dim3(4 * kWave), 0, stream, xq,
                            wq, M, N, K, ep);
@@ -776,6 +808,14 @@ hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t*
             go(std::integral_constant<int, 3>{});
         else
             go(std::integral_constant<int, 4>{});
+    } else if (p.cols > 0) {
+        launch_tile<Tile256, kTileFinal>(M, p.cols, K, 1, K, kTiles[0].group, xq, wq, nullptr, ep,
+                                         stream);
+        with_tile(p.rest, [&](auto shape) {
+            launch_tile<decltype(shape), kTileFinal>(M, N - p.cols, K, 1, K, kTiles[p.rest].group, xq,
+                                                     wq + (int64_t)p.cols * K, nullptr,
+                                                     columns_from(ep, p.cols), stream);
+        });
     } else {
         with_tile(p.tile, [&](auto shape) {
             launch_split<decltype(shape)>(M, N, K, p.S, p.kc, kTiles[p.tile].group, xq, wq, ws, ep,
@@ -785,18 +825,32 @@ hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t*
     return hipGetLastError();
 }
 
+Int8Launches int8_launches(int M, int N, int K) {
+    const Int8Plan p = int8_plan(M, N, K);
+    return Int8Launches{p.cols > 0 ? 2 : 1, p.S > 1 ? 1 : 0};
+}
+
 bool int8_gated_ok(int M, int F, int H) {
     const Int8Plan p = int8_plan(M, 2 * F, H);
     return p.kind == Int8Plan::kTile && p.S == 1;
 }
 
 hipError_t launch_gated_int8(int M, int F, int H, const int8_t* xq, const int8_t* wq,
-                             const Int8Epilogue& ep, hipStream_t stream) {
+                             const Int8Epilogue& epilogue, hipStream_t stream) {
     const Int8Plan p = int8_plan(M, 2 * F, H, true, true);
+    Int8Epilogue ep = epilogue;
+    ep.ld = ep.up = F;
+    const int half = p.cols / 2;  // gated tiles are half as wide in outputs
     with_tile(p.tile, [&](auto shape) {
-        launch_tile<decltype(shape), kTileGated>(M, F, H, 1, H, kTiles[p.tile].group, xq, wq,
-                                                 nullptr, ep, stream);
+        launch_tile<decltype(shape), kTileGated>(M, half > 0 ? half : F, H, 1, H, kTiles[p.tile].group,
+                                                 xq, wq, nullptr, ep, stream);
     });
+    if (half > 0)
+        with_tile(p.rest, [&](auto shape) {
+            launch_tile<decltype(shape), kTileGated>(M, F - half, H, 1, H, kTiles[p.rest].group, xq,
+                                                     wq + (int64_t)half * H, nullptr,
+                                                     columns_from(ep, half), stream);
+        });
     return hipGetLastError();
 }
 

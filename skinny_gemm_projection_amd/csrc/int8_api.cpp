@@ -131,10 +131,12 @@ sg_status skinny_gemm_int8(int32_t M, int32_t N, int32_t K, const int8_t* x_code
     if (sg::launch_gemm_int8(M, N, K, x_codes, W_codes, ep, workspace,
                              static_cast<hipStream_t>(stream)) != hipSuccess)
         return SG_ERR_HIP;
-    sg::count_launch(SG_KERNEL_INT8);
+    const sg::Int8Launches n = sg::int8_launches(M, N, K);
+    for (int i = 0; i < n.main; ++i) sg::count_launch(SG_KERNEL_INT8);
+    for (int i = 0; i < n.reduce; ++i) sg::count_launch(SG_KERNEL_REDUCE);
     if (sg::launch_log_enabled())
-        std::fprintf(stderr, "[skinny_gemm] int8 M=%d N=%d K=%d%s\n", M, N, K,
-                     r ? " residual" : "");
+        std::fprintf(stderr, "[skinny_gemm] int8 M=%d N=%d K=%d launches=%d%s%s\n", M, N, K, n.main,
+                     n.reduce ? " +reduce pass" : "", r ? " residual" : "");
     return SG_OK;
 }
 
@@ -181,7 +183,11 @@ sg_status skinny_mlp_int8_step(const sg_mlp_int8_step* a, void* workspace, size_
         if (sg::launch_gated_int8(a->M, a->F, a->H, q, a->W_gate_up, ep,
                                   static_cast<hipStream_t>(stream)) != hipSuccess)
             return SG_ERR_HIP;
-        sg::count_launch(SG_KERNEL_INT8);
+        const int n = sg::int8_launches(a->M, 2 * a->F, a->H).main;
+        for (int i = 0; i < n; ++i) sg::count_launch(SG_KERNEL_INT8);
+        if (sg::launch_log_enabled())
+            std::fprintf(stderr, "[skinny_gemm] int8 gated M=%d F=%d H=%d launches=%d\n", a->M, a->F,
+                         a->H, n);
         st = skinny_quant_int8(a->M, a->F, nullptr, u, 0, p, sp, stream);
     } else {
         st = skinny_gemm_int8(a->M, 2 * a->F, a->H, q, sq, a->W_gate_up, a->gate_up_scales,

@@ -186,8 +186,14 @@ struct Int8Epilogue {
     float* y_f32;         // nullable
     uint16_t* y_bf16;     // nullable; may equal r
     const uint16_t* r;    // residual [M, N] or nullptr
+    int ld = 0;           // row stride of the outputs and the residual (set by the launchers)
+    int up = 0;           // gated: rows of W (and scales) from a gate row to its up row
 };
 size_t int8_workspace_bytes(int M, int N, int K);
+struct Int8Launches {
+    int main, reduce;  // kernels that launch_gemm_int8 enqueues
+};
+Int8Launches int8_launches(int M, int N, int K);
 // The gated product in the epilogue of the gate and up projections: y_f32
 // [M, F] = silu(x Wg^T) * (x Wu^T) for wq [2F, H] (gate rows, then up rows) and
 // its scales, F a multiple of 16; where int8_gated_ok, the same bits as the

@@ -61,7 +61,9 @@ GEMM = [(1, 1, 16), (1, 40, 16), (1, 129, 112), (1, 1024, 1024), (1, 200, 8208),
         (4097, 17, 3088), (3000, 64, 4112),
         # row pitches of a multiple of 4 KB: every workgroup starts elsewhere in K
         (1, 300, 4096), (16, 1000, 8192), (3, 8200, 4096), (20, 8195, 4096), (5, 20001, 4096),
-        (40, 500, 12288), (50, 100, 4096), (2, 17, 16384)]
+        (40, 500, 12288), (50, 100, 4096), (2, 17, 16384),
+        # two launches: whole rounds of the largest tiles, smaller ones for the other columns
+        (1281, 12290, 528), (1281, 12292, 528)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)
@@ -76,7 +78,10 @@ def test_gemm_bits(M, N, K):
     before = sg.skinny_gemm_get_counters()
     sg.skinny_gemm_int8(*d[:4], y_f32=y32, y_bf16=y16)
     torch.cuda.synchronize()
-    assert counters_delta(before, sg.skinny_gemm_get_counters())[sg.SG_KERNEL_INT8] == 1
+    ran = counters_delta(before, sg.skinny_gemm_get_counters())
+    assert ran[sg.SG_KERNEL_INT8] in (1, 2)  # two: whole rounds of tiles, then the other columns
+    assert ran[sg.SG_KERNEL_REDUCE] == (1 if sg.skinny_gemm_int8_workspace(M, N, K) else 0)
+    assert sum(ran) == ran[sg.SG_KERNEL_INT8] + ran[sg.SG_KERNEL_REDUCE]
     want = ref.linear(xq, xs, wq, ws)
     same(y32, want, "fp32")
     same(y16, want.to(BF16), "bf16")
@@ -339,7 +344,8 @@ def parts(x, r, g, wgu, sgu, wd, sd):
 MLP = [(1, 512, 1024), (1, 16, 16), (2, 7168, 2064), (4, 1040, 2064), (16, 528, 272), (33, 272, 1040),
        (61, 1024, 4112), (65, 528, 1040), (130, 1040, 784), (300, 512, 1296), (1025, 272, 528),
        # every tile size with the gated product in its epilogue
-       (65, 272, 8208), (129, 144, 8208), (257, 144, 12304), (400, 272, 8208)]
+       (65, 272, 8208), (129, 144, 8208), (257, 144, 12304), (400, 272, 8208),
+       (1281, 528, 6160)]
 
 
 @pytest.mark.parametrize("M,H,F", MLP)
