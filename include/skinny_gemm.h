@@ -304,9 +304,9 @@ size_t skinny_gemm_mxfp4_workspace(int32_t M, int32_t N, int32_t K);
  * gated MLP block of them.  They serve batches of any size up to SG_INT8_MAX_M
  * rows: a caller that holds int8 weights has no other path for its prompts.
  *
- * Codes of a row v[0..K): amax = max_k |v[k]|, code[k] = round-half-even(v[k]
- * * (127 / amax)) in fp32, scale = amax / 127 (so v is about code * scale;
- * codes lie in [-127, 127]).  A row of zeros has codes 0 and scale 0.  A row
+ * Codes of a row v[0..K): amax = max_k |v[k]|, code[k] = v[k] * (127 / amax)
+ * rounded once, half to even (the quotient in fp32), scale = amax / 127 (so v is
+ * about code * scale; codes lie in [-127, 127]).  A row of zeros has codes 0 and scale 0.  A row
  * that holds a NaN or an infinity (or whose fp32 intermediates overflow) has
  * codes 0 and scale NaN, so everything computed from it is NaN.
  * Rows never depend on each other, and repeated calls give identical bits. */
@@ -334,7 +334,9 @@ sg_status skinny_rmsnorm(int32_t M, int32_t K, const sg_bf16* x, const sg_bf16* 
  * (exactly one non-NULL).  gated == 0: x [M, K], v = x -- activations in front
  * of an integer projection, or (M = N) the channels of a weight matrix.
  * gated == 1: x [M, 2K] holds gate rows then up rows, v = silu(gate) * up =
- * gate / (1 + exp(-gate)) * up in fp32, not rounded before the codes.
+ * gate / (1 + exp(-gate)) * up in fp32, not rounded before the codes; the
+ * exponential and the reciprocal are the hardware's (off by at most one step
+ * each), and a gate below about -87 gives 0.
  * Limits: 0 <= M <= SG_INT8_MAX_M, 1 <= K <= SG_ROW_MAX_K, gated 0 or 1 (else
  * SG_ERR_SHAPE); K % 8 == 0, pointers 16-byte aligned (scales 4-byte) (else
  * SG_ERR_ALIGN).  Outputs must not overlap x. */
@@ -349,7 +351,8 @@ sg_status skinny_quant_int8(int32_t M, int32_t K, const sg_bf16* x_bf16, const f
  * [M, N] gives the fused residual bf16_RNE(fp32(r) + y), y_bf16 may equal r.
  * A NaN or infinite scale follows fp32's rules (0 * infinity is NaN).
  * workspace: skinny_gemm_int8_workspace bytes (16-byte aligned; NULL when
- * that is 0), for the int32 partial sums of a K split between workgroups.
+ * that is 0), for the int32 partial sums of a K split between workgroups;
+ * calls that may overlap in time (other streams, other graphs) need one each.
  * Limits: 0 <= M <= SG_INT8_MAX_M, 0 <= N <= 1<<20, 0 <= K <= SG_INT8_MAX_K
  * (else SG_ERR_SHAPE); K % 16 == 0, codes, r, outputs and workspace 16-byte
  * aligned, scales 4-byte (else SG_ERR_ALIGN). */
@@ -373,7 +376,9 @@ size_t skinny_gemm_int8_workspace(int32_t M, int32_t N, int32_t K);
  * SG_ROW_MAX_K, eps positive and finite (else SG_ERR_SHAPE); H % 16 == 0,
  * F % 16 == 0, pointers 16-byte aligned (scales 4-byte) (else SG_ERR_ALIGN).
  * Workspace: skinny_mlp_int8_step_workspace bytes, 16-byte aligned, holds the
- * codes, scales and u between the launches. */
+ * codes, scales and u between the launches; one for each call that may overlap
+ * in time.  At prompt sizes the gated product is taken in the projection's
+ * epilogue: same bits, u is [M, F]. */
 typedef struct {
     const sg_bf16* x;
     const sg_bf16* r;
