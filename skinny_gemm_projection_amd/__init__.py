@@ -12,6 +12,7 @@ built, importing it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -392,25 +393,29 @@ def _ws_arg(workspace, nbytes, dev, stream):
     return workspace, _ptr(workspace, torch.uint8, "workspace", dev), workspace.numel()
 
 
-def _raw_current():
-    """The functions behind torch.cuda.current_stream and current_device, without the Stream
-    object and the initialisation check that cost more host time than all checks of a call
-    (its tensors are on the device already, so the runtime is up)."""
-    return torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# The functions behind torch.cuda.current_stream and current_device, without the Stream object
+# and the initialisation check, which cost more host time than all checks of a call (its tensors
+# are on the device already, so the runtime is up).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_device = torch._C._cuda_getDevice
 
 
 def _run_on(dev, stream, fn, *args):
     """fn(*args, stream handle) with dev current; the default stream is dev's current one."""
-    raw_stream, raw_device = _raw_current()
     index = dev.index
-    handle = raw_stream(index) if stream is None else _stream(stream)
-    if raw_device() == index:
+    handle = _raw_stream(index) if stream is None else _stream(stream)
+    if _raw_device() == index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
             st = fn(*args, handle)
     if st:
         _lib.check(st)
+
+
+@functools.lru_cache(maxsize=4096)
+def _gemm_int8_workspace(M, N, K):
+    return _c().skinny_gemm_int8_workspace(M, N, K)
 
 
 def skinny_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, r=None, h=None, y_bf16=None,
@@ -473,11 +478,10 @@ def skinny_gemm_int8(x_codes: torch.Tensor, x_scales: torch.Tensor, W_codes: tor
     M, K, dev, px = _rows(x_codes, "x_codes", (i8,))
     N = W_codes.shape[0]
     mn = (M, N)
-    c = _c()
     if y_f32 is None and y_bf16 is None:
         y_f32 = _new(mn, torch.float32, dev, stream)
-    ws, ws_ptr, ws_bytes = _ws_arg(workspace, c.skinny_gemm_int8_workspace(M, N, K), dev, stream)
-    _run_on(dev, stream, c.skinny_gemm_int8, M, N, K, px,
+    ws, ws_ptr, ws_bytes = _ws_arg(workspace, _gemm_int8_workspace(M, N, K), dev, stream)
+    _run_on(dev, stream, _c().skinny_gemm_int8, M, N, K, px,
             _arg(x_scales, f32, (M,), "x_scales", dev), _arg(W_codes, i8, (N, K), "W_codes", dev),
             _arg(W_scales, f32, (N,), "W_scales", dev),
             None if r is None else _arg(r, bf16, mn, "r", dev),

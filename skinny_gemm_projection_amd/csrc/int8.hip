@@ -692,15 +692,9 @@ constexpr int kCus = 256;
 constexpr int kTeamMaxM = 64;
 constexpr double kStreamBytesPerUs = 5.6e6;  // W from HBM through the tile kernel
 
-struct Int8Plan {
-    enum Kind { kTeam, kWide, kTile } kind;
-    int waves, rt, slots;  // team kernel
-    int tile, S, kc;       // tile kernel: variant, K splits, codes a split
-    size_t workspace;
-    int cols, rest;        // columns of the first launch (0: all), variant of the others' tiles
-};
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
 
 // The variant with the least estimated time (us).  Team: 2 us, then 0.038 us
 // per KB of W and 0.012 (0.016 past 48 rows) per KB of x that a compute unit
@@ -708,10 +702,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // code, but no faster than W comes from HBM; a split adds the reduction's
 // launch and its traffic.  Over 38 shapes of 1 to 4096 rows the choice was
 // within 3 % of the fastest variant on average.
-Int8Plan int8_plan(int M, int N, int K, bool tiles_only = false, bool one_split = false) {
+Int8Plan int8_plan(int M, int N, int K) {
     Int8Plan best{};
     double least = 1e30;
-    if (!tiles_only && M <= kTeamMaxM) {
+    if (M <= kTeamMaxM) {
         for (int rt = 1; rt <= (M <= 48 ? 2 : 1); ++rt) {
             const double wgs = (double)ceil_div(N, 16 * rt);
             const double per = wgs > kCus ? wgs / kCus : 1.0;
@@ -743,7 +737,7 @@ Int8Plan int8_plan(int M, int N, int K, bool tiles_only = false, bool one_split 
     for (int v = 0; v < kTileVariants; ++v) {
         const TileCost& c = kTiles[v];
         const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn);
-        for (int S = 1; S <= (one_split ? 1 : 16); ++S) {
+        for (int S = 1; S <= 16; ++S) {
             const int kc = S == 1 ? K : (int)ceil_div(ceil_div(K, S), kStageK) * kStageK;
             if (S > 1 && (kc < 4 * kStageK || (int64_t)(S - 1) * kc >= K)) break;
             double est = tiles_us(v, N, S, kc);
@@ -774,10 +768,6 @@ Int8Plan int8_plan(int M, int N, int K, bool tiles_only = false, bool one_split 
     return best;
 }
 
-}  // namespace
-
-size_t int8_workspace_bytes(int M, int N, int K) { return int8_plan(M, N, K).workspace; }
-
 // The outputs and weights from column `cols` on.
 static Int8Epilogue columns_from(const Int8Epilogue& ep, int cols) {
     Int8Epilogue e = ep;
@@ -788,9 +778,9 @@ static Int8Epilogue columns_from(const Int8Epilogue& ep, int cols) {
     return e;
 }
 
-hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t* wq,
-                            const Int8Epilogue& epilogue, void* ws, hipStream_t stream) {
-    const Int8Plan p = int8_plan(M, N, K);
+hipError_t launch_gemm_int8(const Int8Plan& p, int M, int N, int K, const int8_t* xq,
+                            const int8_t* wq, const Int8Epilogue& epilogue, void* ws,
+                            hipStream_t stream) {
     Int8Epilogue ep = epilogue;
     ep.ld = N;
     if (p.kind == Int8Plan::kWide) {
@@ -825,19 +815,10 @@ hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t*
     return hipGetLastError();
 }
 
-Int8Launches int8_launches(int M, int N, int K) {
-    const Int8Plan p = int8_plan(M, N, K);
-    return Int8Launches{p.cols > 0 ? 2 : 1, p.S > 1 ? 1 : 0};
-}
+bool int8_gated_ok(const Int8Plan& p) { return p.kind == Int8Plan::kTile && p.S == 1; }
 
-bool int8_gated_ok(int M, int F, int H) {
-    const Int8Plan p = int8_plan(M, 2 * F, H);
-    return p.kind == Int8Plan::kTile && p.S == 1;
-}
-
-hipError_t launch_gated_int8(int M, int F, int H, const int8_t* xq, const int8_t* wq,
-                             const Int8Epilogue& epilogue, hipStream_t stream) {
-    const Int8Plan p = int8_plan(M, 2 * F, H, true, true);
+hipError_t launch_gated_int8(const Int8Plan& p, int M, int F, int H, const int8_t* xq,
+                             const int8_t* wq, const Int8Epilogue& epilogue, hipStream_t stream) {
     Int8Epilogue ep = epilogue;
     ep.ld = ep.up = F;
     const int half = p.cols / 2;  // gated tiles are half as wide in outputs

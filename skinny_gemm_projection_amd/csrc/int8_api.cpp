@@ -30,7 +30,9 @@ bool rows_ok(int32_t M, int32_t K) {
 
 // Byte offsets of the MLP step's intermediates in its workspace.
 struct MlpLayout {
-    size_t q, sq, u, p, sp, gemm, gemm_bytes, total;
+    size_t q, sq, u, p, sp, gemm, total;
+    sg::Int8Plan up, down;  // the two products
+    bool gated;             // the gated product is taken in the first one's epilogue
 };
 
 bool mlp_layout(int32_t M, int32_t H, int32_t F, MlpLayout* L) {
@@ -47,15 +49,32 @@ bool mlp_layout(int32_t M, int32_t H, int32_t F, MlpLayout* L) {
     L->q = take(m * H);
     L->sq = take(m * 4);
     // the projections' outputs, or (gated in the epilogue) the gated product alone
-    L->u = take(m * F * (M > 0 && sg::int8_gated_ok(M, F, H) ? 4 : 8));
+    L->up = sg::int8_plan(M > 0 ? M : 1, 2 * F, H);
+    L->down = sg::int8_plan(M > 0 ? M : 1, H, F);
+    L->gated = sg::int8_gated_ok(L->up);
+    L->u = take(m * F * (L->gated ? 4 : 8));
     L->p = take(m * F);
     L->sp = take(m * 4);
-    const size_t a = M > 0 ? sg::int8_workspace_bytes(M, 2 * F, H) : 0;
-    const size_t b = M > 0 ? sg::int8_workspace_bytes(M, H, F) : 0;
-    L->gemm_bytes = a > b ? a : b;
-    L->gemm = take(L->gemm_bytes);
+    const size_t a = L->up.workspace, b = L->down.workspace;
+    L->gemm = take(M == 0 ? 0 : a > b ? a : b);
     L->total = at;
     return true;
+}
+
+// The launches of one checked product, counted and logged.
+sg_status product(const sg::Int8Plan& p, int32_t M, int32_t N, int32_t K, const int8_t* xq,
+                  const float* xs, const int8_t* wq, const float* ws, const sg_bf16* r, float* y_f32,
+                  sg_bf16* y_bf16, void* workspace, hipStream_t stream) {
+    (void)hipGetLastError();
+    const sg::Int8Epilogue ep{xs, ws, y_f32, y_bf16, r};
+    if (sg::launch_gemm_int8(p, M, N, K, xq, wq, ep, workspace, stream) != hipSuccess)
+        return SG_ERR_HIP;
+    for (int i = 0; i < p.launches(); ++i) sg::count_launch(SG_KERNEL_INT8);
+    if (p.workspace > 0) sg::count_launch(SG_KERNEL_REDUCE);
+    if (sg::launch_log_enabled())
+        std::fprintf(stderr, "[skinny_gemm] int8 M=%d N=%d K=%d launches=%d%s%s\n", M, N, K,
+                     p.launches(), p.workspace > 0 ? " +reduce pass" : "", r ? " residual" : "");
+    return SG_OK;
 }
 
 }  // namespace
@@ -106,7 +125,7 @@ sg_status skinny_quant_int8(int32_t M, int32_t K, const sg_bf16* x_bf16, const f
 
 size_t skinny_gemm_int8_workspace(int32_t M, int32_t N, int32_t K) {
     if (!gemm_sizes_ok(M, N, K) || K % 16 != 0 || M == 0 || N == 0) return 0;
-    return sg::int8_workspace_bytes(M, N, K);
+    return sg::int8_plan(M, N, K).workspace;
 }
 
 sg_status skinny_gemm_int8(int32_t M, int32_t N, int32_t K, const int8_t* x_codes,
@@ -121,23 +140,13 @@ sg_status skinny_gemm_int8(int32_t M, int32_t N, int32_t K, const int8_t* x_code
     if (!aligned16(x_codes) || !aligned16(W_codes) || !aligned4(x_scales) || !aligned4(W_scales) ||
         !aligned16(r) || !aligned16(y_f32) || !aligned16(y_bf16))
         return SG_ERR_ALIGN;
-    const size_t need = sg::int8_workspace_bytes(M, N, K);
-    if (need > 0) {
-        if (!workspace || workspace_bytes < need) return SG_ERR_WORKSPACE;
+    const sg::Int8Plan plan = sg::int8_plan(M, N, K);
+    if (plan.workspace > 0) {
+        if (!workspace || workspace_bytes < plan.workspace) return SG_ERR_WORKSPACE;
         if (!aligned16(workspace)) return SG_ERR_ALIGN;
     }
-    (void)hipGetLastError();
-    const sg::Int8Epilogue ep{x_scales, W_scales, y_f32, y_bf16, r};
-    if (sg::launch_gemm_int8(M, N, K, x_codes, W_codes, ep, workspace,
-                             static_cast<hipStream_t>(stream)) != hipSuccess)
-        return SG_ERR_HIP;
-    const sg::Int8Launches n = sg::int8_launches(M, N, K);
-    for (int i = 0; i < n.main; ++i) sg::count_launch(SG_KERNEL_INT8);
-    for (int i = 0; i < n.reduce; ++i) sg::count_launch(SG_KERNEL_REDUCE);
-    if (sg::launch_log_enabled())
-        std::fprintf(stderr, "[skinny_gemm] int8 M=%d N=%d K=%d launches=%d%s%s\n", M, N, K, n.main,
-                     n.reduce ? " +reduce pass" : "", r ? " residual" : "");
-    return SG_OK;
+    return product(plan, M, N, K, x_codes, x_scales, W_codes, W_scales, r, y_f32, y_bf16, workspace,
+                   static_cast<hipStream_t>(stream));
 }
 
 size_t skinny_mlp_int8_step_workspace(int32_t M, int32_t H, int32_t F) {
@@ -172,31 +181,29 @@ sg_status skinny_mlp_int8_step(const sg_mlp_int8_step* a, void* workspace, size_
     int8_t* p = reinterpret_cast<int8_t*>(base + L.p);
     float* sp = reinterpret_cast<float*>(base + L.sp);
     void* gw = base + L.gemm;
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
     sg_status st;
     // out holds h between the norm and the down projection, which adds to it
     if ((st = skinny_rmsnorm(a->M, a->H, a->x, a->r, a->g, a->eps, a->out, nullptr, q, sq,
                              stream)) != SG_OK)
         return st;
-    if (sg::int8_gated_ok(a->M, a->F, a->H)) {
+    if (L.gated) {
         // long prompts: the gated product leaves the projection's epilogue, u is [M, F]
         const sg::Int8Epilogue ep{sq, a->gate_up_scales, u, nullptr, nullptr};
-        if (sg::launch_gated_int8(a->M, a->F, a->H, q, a->W_gate_up, ep,
-                                  static_cast<hipStream_t>(stream)) != hipSuccess)
+        if (sg::launch_gated_int8(L.up, a->M, a->F, a->H, q, a->W_gate_up, ep, hs) != hipSuccess)
             return SG_ERR_HIP;
-        const int n = sg::int8_launches(a->M, 2 * a->F, a->H).main;
-        for (int i = 0; i < n; ++i) sg::count_launch(SG_KERNEL_INT8);
+        for (int i = 0; i < L.up.launches(); ++i) sg::count_launch(SG_KERNEL_INT8);
         if (sg::launch_log_enabled())
             std::fprintf(stderr, "[skinny_gemm] int8 gated M=%d F=%d H=%d launches=%d\n", a->M, a->F,
-                         a->H, n);
-        st = skinny_quant_int8(a->M, a->F, nullptr, u, 0, p, sp, stream);
-    } else {
-        st = skinny_gemm_int8(a->M, 2 * a->F, a->H, q, sq, a->W_gate_up, a->gate_up_scales,
-                              nullptr, u, nullptr, gw, L.gemm_bytes, stream);
-        if (st == SG_OK) st = skinny_quant_int8(a->M, a->F, nullptr, u, 1, p, sp, stream);
+                         a->H, L.up.launches());
+    } else if ((st = product(L.up, a->M, 2 * a->F, a->H, q, sq, a->W_gate_up, a->gate_up_scales,
+                             nullptr, u, nullptr, gw, hs)) != SG_OK) {
+        return st;
     }
-    if (st != SG_OK) return st;
-    return skinny_gemm_int8(a->M, a->H, a->F, p, sp, a->W_down, a->down_scales, a->out, nullptr,
-                            a->out, gw, L.gemm_bytes, stream);
+    if ((st = skinny_quant_int8(a->M, a->F, nullptr, u, L.gated ? 0 : 1, p, sp, stream)) != SG_OK)
+        return st;
+    return product(L.down, a->M, a->H, a->F, p, sp, a->W_down, a->down_scales, a->out, nullptr,
+                   a->out, gw, hs);
 }
 
 }  // extern "C"

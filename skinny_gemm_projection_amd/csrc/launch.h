@@ -189,20 +189,25 @@ struct Int8Epilogue {
     int ld = 0;           // row stride of the outputs and the residual (set by the launchers)
     int up = 0;           // gated: rows of W (and scales) from a gate row to its up row
 };
-size_t int8_workspace_bytes(int M, int N, int K);
-struct Int8Launches {
-    int main, reduce;  // kernels that launch_gemm_int8 enqueues
+// What runs for a size: the kernel form with the least estimated time.
+struct Int8Plan {
+    enum Kind { kTeam, kWide, kTile } kind;
+    int waves, rt, slots;  // team kernel
+    int tile, S, kc;       // tile kernel: variant, K splits, codes a split
+    size_t workspace;      // bytes of int32 partial sums (S > 1)
+    int cols, rest;        // columns of the first launch (0: all), variant of the others' tiles
+    int launches() const { return cols > 0 ? 2 : 1; }  // the reduction of a split apart
 };
-Int8Launches int8_launches(int M, int N, int K);
+Int8Plan int8_plan(int M, int N, int K);
+hipError_t launch_gemm_int8(const Int8Plan& p, int M, int N, int K, const int8_t* xq,
+                            const int8_t* wq, const Int8Epilogue& ep, void* ws, hipStream_t stream);
 // The gated product in the epilogue of the gate and up projections: y_f32
 // [M, F] = silu(x Wg^T) * (x Wu^T) for wq [2F, H] (gate rows, then up rows) and
-// its scales, F a multiple of 16; where int8_gated_ok, the same bits as the
-// separate calls give.
-bool int8_gated_ok(int M, int F, int H);
-hipError_t launch_gated_int8(int M, int F, int H, const int8_t* xq, const int8_t* wq,
-                             const Int8Epilogue& ep, hipStream_t stream);
-hipError_t launch_gemm_int8(int M, int N, int K, const int8_t* xq, const int8_t* wq,
-                            const Int8Epilogue& ep, void* ws, hipStream_t stream);
+// its scales, F a multiple of 16, by the plan of M x 2F x H where that is one of
+// whole tiles (int8_gated_ok); the same bits as the separate calls give.
+bool int8_gated_ok(const Int8Plan& p);
+hipError_t launch_gated_int8(const Int8Plan& p, int M, int F, int H, const int8_t* xq,
+                             const int8_t* wq, const Int8Epilogue& ep, hipStream_t stream);
 
 // Router top-k: ids [T,k] (and their scores) from fp32 scores, row t at
 // scores + t*ld (ld >= E); E <= 4096, k <= 32 (checked by the caller).
