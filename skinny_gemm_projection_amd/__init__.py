@@ -363,14 +363,16 @@ def _rows(x, name, dtypes):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(x).__name__}")
     if x.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
-    if not x.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor")
-    if not x.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
     try:
         M, K = x.shape
     except ValueError:
         raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(x.shape)}") from None
+    if M > 0x7fffffff or K > 0x7fffffff:  # the C ABI's sizes are int32 and would wrap around
+        raise ValueError(f"{name}: shape {tuple(x.shape)} is past 2^31 - 1")
+    if not x.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
     return M, K, x.device, x.data_ptr()
 
 
@@ -476,13 +478,15 @@ def skinny_gemm_int8(x_codes: torch.Tensor, x_scales: torch.Tensor, W_codes: tor
     none is given; returns the outputs."""
     i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
     M, K, dev, px = _rows(x_codes, "x_codes", (i8,))
-    N = W_codes.shape[0]
+    N, _, _, pw = _rows(W_codes, "W_codes", (i8,))
+    if W_codes.shape[1] != K or W_codes.get_device() != dev.index:
+        _arg(W_codes, i8, (N, K), "W_codes", dev)  # raises
     mn = (M, N)
     if y_f32 is None and y_bf16 is None:
         y_f32 = _new(mn, torch.float32, dev, stream)
     ws, ws_ptr, ws_bytes = _ws_arg(workspace, _gemm_int8_workspace(M, N, K), dev, stream)
     _run_on(dev, stream, _c().skinny_gemm_int8, M, N, K, px,
-            _arg(x_scales, f32, (M,), "x_scales", dev), _arg(W_codes, i8, (N, K), "W_codes", dev),
+            _arg(x_scales, f32, (M,), "x_scales", dev), pw,
             _arg(W_scales, f32, (N,), "W_scales", dev),
             None if r is None else _arg(r, bf16, mn, "r", dev),
             None if y_f32 is None else _arg(y_f32, f32, mn, "y_f32", dev),

@@ -142,3 +142,14 @@ def test_binding_refuses_what_the_library_cannot_see():
         sg.skinny_quant_int8(x[:, :31], gated=True, codes=q, scales=s)
     with pytest.raises(TypeError):
         sg.skinny_mlp_int8_step(x.half(), g, 1e-6, q, s, w, t, out=x)
+
+
+def test_binding_refuses_sizes_past_int32():
+    """The library's sizes are 32-bit: a longer tensor is refused, not taken modulo 2^32."""
+    long, s = torch.empty((2 ** 32 + 8, 0), dtype=torch.int8), torch.ones(8)
+    w, x, g = torch.empty((8, 0), dtype=torch.int8), long.bfloat16(), s.bfloat16()
+    for call in (lambda: sg.skinny_gemm_int8(long, s, w, s), lambda: sg.skinny_quant_int8(x),
+                 lambda: sg.skinny_rmsnorm(x, g, 1e-6),
+                 lambda: sg.skinny_mlp_int8_step(x, g, 1e-6, w, s, w, s)):
+        with pytest.raises(ValueError, match="past 2"):
+            call()
