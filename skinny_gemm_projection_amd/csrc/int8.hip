@@ -55,13 +55,6 @@ __device__ __forceinline__ void load_to_lds(rsrc_t r, uint4* lds, uint32_t offse
 // Before a wave refills an LDS slot of its own: its reads of the slot are done.
 __device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// Between LDS writes and reads of other lanes' data inside one wave.
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // y of four neighbouring outputs: one rounding for the conversion and each product
 __device__ __forceinline__ void scale4(const i32x4_t acc, const float4 ws, float xs, float (&y)[4]) {
 #pragma clang fp contract(off)
@@ -71,23 +64,29 @@ __device__ __forceinline__ void scale4(const i32x4_t acc, const float4 ws, float
     y[3] = (float)acc[3] * ws.w * xs;
 }
 
-// Outputs y[m][n .. n+4) with the residual; rows of a multiple of 4 elements
-// keep the four together.
+// Outputs y[m][n .. n+4) with the residual, one access each way also where rows
+// of y are not 4-element aligned: global memory takes any alignment.  (333 x 5001
+// x 2064: 10.9 us, as for 5008 columns; four scalar stores a lane 15.5, rows
+// turned in LDS and stored an element a lane 12.3.)
 __device__ __forceinline__ void finish4(const Int8Epilogue& ep, int N, int m, int n, float (&y)[4]) {
     const int64_t at = (int64_t)m * ep.ld + n;
-    if ((ep.ld & 3) == 0) {
+    if (n + 4 <= N) {
         if (ep.r) {
-            const uint2 r = *reinterpret_cast<const uint2*>(ep.r + at);
+            uint2 r;
+            __builtin_memcpy(&r, ep.r + at, 8);
             y[0] = as_f(r.x << 16) + y[0];
             y[1] = as_f(r.x & 0xffff0000u) + y[1];
             y[2] = as_f(r.y << 16) + y[2];
             y[3] = as_f(r.y & 0xffff0000u) + y[3];
         }
-        if (ep.y_f32)
-            *reinterpret_cast<float4*>(ep.y_f32 + at) = make_float4(y[0], y[1], y[2], y[3]);
-        if (ep.y_bf16)
-            *reinterpret_cast<uint2*>(ep.y_bf16 + at) =
-                make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+        if (ep.y_f32) {
+            const float4 v = make_float4(y[0], y[1], y[2], y[3]);
+            __builtin_memcpy(ep.y_f32 + at, &v, 16);
+        }
+        if (ep.y_bf16) {
+            const uint2 v = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+            __builtin_memcpy(ep.y_bf16 + at, &v, 8);
+        }
     } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -97,26 +96,6 @@ __device__ __forceinline__ void finish4(const Int8Epilogue& ep, int N, int m, in
             if (ep.y_f32) ep.y_f32[at + v] = o;
             if (ep.y_bf16) ep.y_bf16[at + v] = f32_to_bf16(o);
         }
-    }
-}
-
-// A 16 x COLS block of finished values whose rows are not 4-element aligned in
-// memory: turned in LDS so that neighbouring lanes write neighbouring elements.
-// (Four scalar stores a lane instead took 333 x 5001 x 2064 from 13.3 to 15.5 us.)
-template <int COLS>
-__device__ __forceinline__ void finish_block(const Int8Epilogue& ep, int M, int N, int m0, int n0,
-                                             const float* block, int lane) {
-    constexpr int kRows = kWave / COLS;  // rows a store instruction covers
-    const int col = lane % COLS, n = n0 + col;
-#pragma unroll
-    for (int r = 0; r < 16; r += kRows) {
-        const int row = r + lane / COLS, m = m0 + row;
-        if (m >= M || n >= N) continue;
-        float y = block[row * (COLS + 4) + col];
-        const int64_t at = (int64_t)m * ep.ld + n;
-        if (ep.r) y = bf16_to_f32(ep.r[at]) + y;
-        if (ep.y_f32) ep.y_f32[at] = y;
-        if (ep.y_bf16) ep.y_bf16[at] = f32_to_bf16(y);
     }
 }
 
@@ -519,27 +498,6 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
             for (int j = 0; j < FM; ++j)
                 if (m0 + (wm * FM + j) * 16 < M)
                     reinterpret_cast<i32x4_t*>(out)[((w * FN + i) * FM + j) * kWave + lane] = acc[i][j];
-    } else if (OUT == kTileFinal && (ep.ld & 3) != 0) {
-        constexpr int kCols = FN * 16;
-        // the stage buffers are free: the last reads were before the last products
-        float* block = reinterpret_cast<float*>(b0) + w * 16 * (kCols + 4);
-        static_assert(T::W * 16 * (kCols + 4) * 4 <= T::kStage * 16, "a block a wave in one buffer");
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-            const int ml = (wm * FM + j) * 16;
-#pragma unroll
-            for (int i = 0; i < FN; ++i) {
-                const int nl = (wn * FN + i) * 16 + grp * 4;
-                float y[4];
-                scale4(acc[i][j], *reinterpret_cast<const float4*>(&sw[nl]), sx[ml + row], y);
-                *reinterpret_cast<float4*>(&block[row * (kCols + 4) + i * 16 + grp * 4]) =
-                    make_float4(y[0], y[1], y[2], y[3]);
-            }
-            wave_lds_fence();
-            finish_block<kCols>(ep, M, N, m0 + ml, n0 + wn * kCols, block, lane);
-            wave_lds_fence();
-        }
     } else {
 #pragma unroll
         for (int j = 0; j < FM; ++j) {

@@ -128,6 +128,25 @@ def test_gemm_scales_that_are_not_finite(M):
     same(h, want.to(BF16), "bf16")
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 5, 16), (3, 8193, 144), (20, 131, 272), (60, 257, 1040),
+                                   (61, 1027, 7168), (200, 6, 144), (333, 1001, 272), (700, 2051, 272)])
+def test_gemm_rows_of_any_alignment(M, N, K):
+    """Rows of y that start at odd elements are written one access for four elements: every
+    element in its place, and nothing behind the last one."""
+    announce(f"int8 odd rows M={M} N={N} K={K}")
+    xq, wq = rand_codes(M, K, 6), rand_codes(N, K, 7)
+    xs, ws = rand_scales(M, 8), rand_scales(N, 9)
+    r = normal((M, N), 10)
+    flat32, flat16 = torch.full((M * N + 16,), -7.0, device=DEV), torch.full((M * N + 16,), -7.0,
+                                                                             device=DEV, dtype=BF16)
+    sg.skinny_gemm_int8(xq.to(DEV), xs.to(DEV), wq.to(DEV), ws.to(DEV), r=r.to(DEV),
+                        y_f32=flat32[:M * N].view(M, N), y_bf16=flat16[:M * N].view(M, N))
+    want = ref.linear(xq, xs, wq, ws, r)
+    for flat, t in ((flat32, torch.float32), (flat16, BF16)):
+        same(flat[:M * N].view(M, N), want.to(t), str(t))
+        assert (flat[M * N:] == -7.0).all(), f"{t}: behind the last element"
+
+
 def test_gemm_empty_sizes():
     f = dict(device=DEV)
     for M, N, K in [(0, 5, 32), (5, 0, 32), (0, 0, 0)]:
