@@ -309,7 +309,10 @@ size_t skinny_gemm_mxfp4_workspace(int32_t M, int32_t N, int32_t K);
  * about code * scale; codes lie in [-127, 127]).  A row of zeros has codes 0 and scale 0.  A row
  * that holds a NaN or an infinity (or whose fp32 intermediates overflow) has
  * codes 0 and scale NaN, so everything computed from it is NaN.
- * Rows never depend on each other, and repeated calls give identical bits. */
+ * Rows never depend on each other, and repeated calls give identical bits.  A
+ * norm adds its squares in an order that follows from K and from whether M is
+ * below 256, so y and its scales may differ in the last bit between such batch
+ * sizes; all else is the same for a row in any batch. */
 #define SG_INT8_MAX_M (1 << 20)
 #define SG_INT8_MAX_K 131056 /* 2^14 * K < 2^31: every sum of products is exact */
 #define SG_ROW_MAX_K 65536   /* a row is held in the registers of one workgroup */
