@@ -337,9 +337,8 @@ sg_status skinny_rmsnorm(int32_t M, int32_t K, const sg_bf16* x, const sg_bf16* 
  * (exactly one non-NULL).  gated == 0: x [M, K], v = x -- activations in front
  * of an integer projection, or (M = N) the channels of a weight matrix.
  * gated == 1: x [M, 2K] holds gate rows then up rows, v = silu(gate) * up =
- * gate / (1 + exp(-gate)) * up in fp32, not rounded before the codes; the
- * exponential and the reciprocal are the hardware's (off by at most one step
- * each), and a gate below about -87 gives 0.
+ * gate / (1 + exp(-gate)) * up in fp32, not rounded before the codes; it is off
+ * by at most 7 * 2^-24 relative, except that a gate below about -87 gives 0.
  * Limits: 0 <= M <= SG_INT8_MAX_M, 1 <= K <= SG_ROW_MAX_K, gated 0 or 1 (else
  * SG_ERR_SHAPE); K % 8 == 0, pointers 16-byte aligned (scales 4-byte) (else
  * SG_ERR_ALIGN).  Outputs must not overlap x. */

@@ -1,0 +1,51 @@
+"""GPU tests of the 8-bit integer operators at the places their other tests leave out: the
+accuracy of the gated product, the kernel forms that long prompts use, every form of a product
+that takes two launches or splits K, and sizes on both sides of the borders between them."""
+import pytest
+import torch
+
+import int8_ref as ref
+import skinny_gemm_projection_amd as sg
+from gpu_common import DEV, announce
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs an MI355X")]
+
+BF16 = torch.bfloat16
+EPS = 1e-6
+
+
+# ------------------------------------------------------------------ gated product
+
+
+@pytest.mark.parametrize("lo,hi", [(-87, -80), (-80, -40), (-40, -20), (-20, -10), (-10, -3), (-3, 0),
+                                   (0, 3), (3, 10), (10, 90), (90, 300)])
+def test_gated_product_error_does_not_grow_with_the_gate(lo, hi):
+    """Rows of one gate and one up value: the scale is the gated product / 127.  exp(-|gate|) is
+    off by 3 u (one step of the hardware's exponential, 2 u, and one rounding), the sum, product,
+    quotient and product with up round once each (4 u), the scale once more."""
+    announce(f"gated product {lo}..{hi}")
+    g = torch.rand(20000, generator=torch.Generator().manual_seed(lo + 100)) * (hi - lo) + lo
+    for u in (1.0, -0.7, 1.0e4):
+        x = torch.cat([g[:, None].expand(-1, 8), torch.full((g.numel(), 8), u)], dim=1).contiguous()
+        codes, scales = sg.skinny_quant_int8(x.to(DEV), gated=True)
+        want = (g.double() * torch.sigmoid(g.double()) * x[:, 8].double()).abs()
+        err = (scales.cpu().double() * 127.0 - want).abs()
+        worst = (err / want.clamp_min(1e-300)).max().item() / ref.U
+        assert (err <= 8 * ref.U * want).all(), f"u = {u}: {worst:.1f} u"
+        assert (codes.abs() == 127).all()
+
+
+def test_gated_product_at_the_ends():
+    """Gates of both zeros, the smallest and largest numbers, below -87 and of both infinities."""
+    tiny, top = 2.0 ** -149, torch.finfo(torch.float32).max
+    g = torch.tensor([0.0, -0.0, tiny, -tiny, top, -top, -104.0, -300.0, float("inf"), float("-inf"),
+                      float("nan")])
+    x = torch.cat([g[:, None].expand(-1, 8), torch.ones(g.numel(), 8)], dim=1).contiguous()
+    codes, scales = [t.cpu() for t in sg.skinny_quant_int8(x.to(DEV), gated=True)]
+    assert (codes[:2] == 0).all() and (scales[:2] == 0).all()
+    assert (scales[2:4] == 0).all()  # 2^-150 and its 127th are below half of the smallest number
+    # (top / 127 is one rounding)
+    assert (codes[4] == 127).all() and abs(scales[4].item() * 127.0 / top - 1) <= 2 * ref.U
+    assert (codes[5:8] == 0).all() and (scales[5:8] == 0).all()
+    assert (codes[8:] == 0).all() and torch.isnan(scales[8:]).all()
