@@ -326,8 +326,8 @@ size_t skinny_gemm_mxfp4_workspace(int32_t M, int32_t N, int32_t K);
  * skinny_gemm_int8; given together).  The codes are those of s * g, from which
  * the row's common factor cancels.  h and y_bf16 may each be the same buffer
  * as x or r (not as one another); any other overlap is undefined.
- * Limits: 0 <= M <= SG_INT8_MAX_M, 1 <= K <= SG_ROW_MAX_K, eps positive and
- * finite (else SG_ERR_SHAPE); K % 8 == 0, pointers 16-byte aligned (scales
+ * Limits: 0 <= M <= SG_INT8_MAX_M, 1 <= K <= SG_ROW_MAX_K, eps finite and at
+ * least 2^-126 (else SG_ERR_SHAPE); K % 8 == 0, pointers 16-byte aligned (scales
  * 4-byte) (else SG_ERR_ALIGN). */
 sg_status skinny_rmsnorm(int32_t M, int32_t K, const sg_bf16* x, const sg_bf16* r,
                          const sg_bf16* g, float eps, sg_bf16* h, sg_bf16* y_bf16, int8_t* codes,
@@ -375,7 +375,7 @@ size_t skinny_gemm_int8_workspace(int32_t M, int32_t N, int32_t K);
  * rows, then up rows) with scales [2F]; W_down [H, F] int8 with scales [H];
  * out [M, H] bf16, which may be x's or r's buffer.  Nothing else may overlap.
  * Limits: 0 <= M <= SG_INT8_MAX_M, 16 <= H <= SG_ROW_MAX_K, 16 <= F <=
- * SG_ROW_MAX_K, eps positive and finite (else SG_ERR_SHAPE); H % 16 == 0,
+ * SG_ROW_MAX_K, eps finite and at least 2^-126 (else SG_ERR_SHAPE); H % 16 == 0,
  * F % 16 == 0, pointers 16-byte aligned (scales 4-byte) (else SG_ERR_ALIGN).
  * Workspace: skinny_mlp_int8_step_workspace bytes, 16-byte aligned, holds the
  * codes, scales and u between the launches; one for each call that may overlap

@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <limits>
 
 #include "launch.h"
 #include "plan_internal.h"
@@ -18,7 +19,9 @@ namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-bool eps_ok(float eps) { return eps > 0.0f && std::isfinite(eps); }
+// Squares below the normal range keep few bits; next to a normal eps that is at
+// most 2^-150 / 2^-126, one rounding, next to a smaller one it would show.
+bool eps_ok(float eps) { return eps >= std::numeric_limits<float>::min() && std::isfinite(eps); }
 
 bool gemm_sizes_ok(int32_t M, int32_t N, int32_t K) {
     return M >= 0 && M <= SG_INT8_MAX_M && N >= 0 && N <= (1 << 20) && K >= 0 && K <= SG_INT8_MAX_K;

@@ -49,3 +49,27 @@ def test_gated_product_at_the_ends():
     assert (codes[4] == 127).all() and abs(scales[4].item() * 127.0 / top - 1) <= 2 * ref.U
     assert (codes[5:8] == 0).all() and (scales[5:8] == 0).all()
     assert (codes[8:] == 0).all() and torch.isnan(scales[8:]).all()
+
+
+# ------------------------------------------------------------------ norm
+
+
+def test_norm_with_the_smallest_eps():
+    """eps = 2^-126 and rows whose squares are below the normal range: adding a square is off by
+    at most 2^-150 there, so the mean by that and by as much again in its own rounding: 2 u of
+    eps, u after the root."""
+    K, eps = 1032, 2.0 ** -126
+    x = torch.randn((60, K), generator=torch.Generator().manual_seed(3))
+    x = (x * 10.0 ** -(17 + torch.arange(60)[:, None] / 6.0)).to(BF16)
+    g = torch.ones(K, dtype=BF16)
+    y = torch.empty((60, K), dtype=BF16, device=DEV)
+    _, _, codes, scales = sg.skinny_rmsnorm(x.to(DEV), g.to(DEV), eps, y_bf16=y,
+                                            codes=torch.empty((60, K), dtype=torch.int8, device=DEV))
+    inv, y64 = ref.norm64(x, None, g, eps)
+    rel = ref.norm_rel(K) + ref.U
+    bound = (2.0 ** -8 + rel + 3 * ref.U) * y64.abs() + 2.0 ** -133
+    assert ((y.cpu().double() - y64).abs() <= bound).all()
+    want, amax, _ = ref.codes_of(x.float())
+    assert torch.equal(codes.cpu(), want)
+    s64 = amax.double() * inv / 127.0
+    assert ((scales.cpu().double() - s64).abs() <= (rel + 3 * ref.U) * s64).all()

@@ -153,3 +153,16 @@ def test_binding_refuses_sizes_past_int32():
                  lambda: sg.skinny_mlp_int8_step(x, g, 1e-6, w, s, w, s)):
         with pytest.raises(ValueError, match="past 2"):
             call()
+
+
+@no_gpu_only
+def test_eps_below_the_normal_range_is_refused():
+    """Squares below the normal range lose bits: with eps there too the norm would be wrong (a
+    row of 2e-23 with eps 2^-149 came out 13 % too large)."""
+    c = _lib.load()
+    for eps in (2.0 ** -149, 1e-40, 2.0 ** -126 * (1 - 2.0 ** -23)):
+        assert c.skinny_rmsnorm(4, 128, A, None, A, eps, None, A, None, None, None) == SHAPE, eps
+        step = _lib.SgMlpInt8Step(x=A, g=A, W_gate_up=A, gate_up_scales=A, W_down=A, down_scales=A,
+                                  out=A, M=4, H=128, F=256, eps=eps)
+        assert c.skinny_mlp_int8_step(ctypes.byref(step), A, 1 << 40, None) == SHAPE, eps
+    assert c.skinny_rmsnorm(0, 128, None, None, None, 2.0 ** -126, None, None, None, None, None) == 0
