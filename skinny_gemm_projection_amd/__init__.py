@@ -397,9 +397,10 @@ def _ws_arg(workspace, nbytes, dev, stream):
 
 # The functions behind torch.cuda.current_stream and current_device, without the Stream object
 # and the initialisation check, which cost more host time than all checks of a call (its tensors
-# are on the device already, so the runtime is up).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_raw_device = torch._C._cuda_getDevice
+# are on the device already, so the runtime is up).  Private names: without them the public ones.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run_on(dev, stream, fn, *args):

@@ -1,6 +1,9 @@
 """Refusals and sizes of the 8-bit integer operators that need no GPU: every call here returns
 before anything is launched."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -12,6 +15,7 @@ no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(),
                                  reason="fake device pointers are only passed on a host without a GPU")
 A = 0x10000  # aligned, never dereferenced
 NULL, SHAPE, ALIGN, WORKSPACE = 1, 2, 4, 5
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(autouse=True)
@@ -166,3 +170,17 @@ def test_eps_below_the_normal_range_is_refused():
                                   out=A, M=4, H=128, F=256, eps=eps)
         assert c.skinny_mlp_int8_step(ctypes.byref(step), A, 1 << 40, None) == SHAPE, eps
     assert c.skinny_rmsnorm(0, 128, None, None, None, 2.0 ** -126, None, None, None, None, None) == 0
+
+
+def test_import_and_sizes_without_torchs_gpu_names():
+    """Plans and workspace sizes are host code: they work on a torch that has no GPU back end,
+    whose torch._C lacks the stream and device functions."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import skinny_gemm_projection_amd as sg\n"
+            "assert sg.skinny_gemm_plan(1, 8192, 7168).M == 1\n"
+            "assert sg.skinny_mlp_int8_step_workspace(1, 64, 64) > 0\n"
+            "print('ok')")
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stderr
