@@ -494,8 +494,14 @@ const char* skinny_gemm_status_str(sg_status status);
 
 /* Launch counters, indexed by sg_kernel: how many times each kernel was
  * launched since load or the last reset ([F] Partie 2 §1: which path ran
- * must be observable).  Process-wide, atomic. */
-void skinny_gemm_get_counters(uint64_t launches[SG_NUM_COUNTERS]);
+ * must be observable).  Process-wide, atomic.  skinny_gemm_read_counters
+ * writes the first n (zeros behind the last one); skinny_gemm_get_counters
+ * writes SG_NUM_COUNTERS, the number in the header that the caller was compiled
+ * with: as a function, without the macro, it writes the 11 that there were
+ * before callers passed their number. */
+void skinny_gemm_read_counters(uint64_t* launches, int32_t n);
+void skinny_gemm_get_counters(uint64_t* launches);
+#define skinny_gemm_get_counters(launches) skinny_gemm_read_counters((launches), SG_NUM_COUNTERS)
 void skinny_gemm_reset_counters(void);
 
 #ifdef __cplusplus

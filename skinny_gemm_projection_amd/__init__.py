@@ -35,7 +35,8 @@ __all__ = [
     "skinny_rmsnorm", "skinny_quant_int8", "skinny_gemm_int8", "skinny_gemm_int8_workspace",
     "skinny_mlp_int8_step", "skinny_mlp_int8_step_workspace",
     "SG_KERNEL_INT8", "SG_KERNEL_RMSNORM", "SG_KERNEL_QUANT_INT8",
-    "skinny_gemm_status_str", "skinny_gemm_get_counters", "skinny_gemm_reset_counters",
+    "skinny_gemm_status_str", "skinny_gemm_read_counters", "skinny_gemm_get_counters",
+    "skinny_gemm_reset_counters",
     "SgPlan", "SkinnyGemmError", "KERNEL_NAMES", "SG_KERNEL_NONE", "SG_KERNEL_GEMV",
     "SG_KERNEL_SPLITK_VALU", "SG_KERNEL_SPLITK_MFMA", "SG_KERNEL_REDUCE", "SG_KERNEL_MOE_TABLE",
     "SG_KERNEL_GROUPED", "SG_KERNEL_PREFETCH", "SG_KERNEL_ROUTER_TOPK", "SG_NUM_COUNTERS",
@@ -600,10 +601,15 @@ def skinny_gemm_status_str(status: int) -> str:
     return _c().skinny_gemm_status_str(status).decode()
 
 
-def skinny_gemm_get_counters() -> list[int]:
-    arr = (ctypes.c_uint64 * SG_NUM_COUNTERS)()
-    _c().skinny_gemm_get_counters(arr)
+def skinny_gemm_read_counters(n: int) -> list[int]:
+    """The first n launch counters, by SG_KERNEL_* (zeros behind the last one)."""
+    arr = (ctypes.c_uint64 * n)()
+    _c().skinny_gemm_read_counters(arr, n)
     return list(arr)
+
+
+def skinny_gemm_get_counters() -> list[int]:
+    return skinny_gemm_read_counters(SG_NUM_COUNTERS)
 
 
 def skinny_gemm_reset_counters() -> None:

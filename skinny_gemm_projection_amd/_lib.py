@@ -130,8 +130,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.skinny_moe_step.argtypes = [ctypes.POINTER(SgMoeStep), p, sz, p, p, p, p]
     lib.skinny_gemm_status_str.argtypes = [ctypes.c_int]
     lib.skinny_gemm_status_str.restype = ctypes.c_char_p
-    lib.skinny_gemm_get_counters.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
-    lib.skinny_gemm_get_counters.restype = None
+    lib.skinny_gemm_read_counters.argtypes = [ctypes.POINTER(ctypes.c_uint64), i32]
+    lib.skinny_gemm_read_counters.restype = None
     lib.skinny_gemm_reset_counters.argtypes = []
     lib.skinny_gemm_reset_counters.restype = None
     for name in ("skinny_gemm_plan", "skinny_gemm_plan_force", "skinny_gemm",

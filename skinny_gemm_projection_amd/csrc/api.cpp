@@ -416,11 +416,15 @@ const char* skinny_gemm_status_str(sg_status status) {
     }
 }
 
-void skinny_gemm_get_counters(uint64_t launches[SG_NUM_COUNTERS]) {
+void skinny_gemm_read_counters(uint64_t* launches, int32_t n) {
     if (!launches) return;
-    for (int i = 0; i < SG_NUM_COUNTERS; ++i)
-        launches[i] = g_launches[i].load(std::memory_order_relaxed);
+    for (int i = 0; i < n; ++i)
+        launches[i] = i < SG_NUM_COUNTERS ? g_launches[i].load(std::memory_order_relaxed) : 0;
 }
+
+// The function itself, which the header's macro of this name does not reach: for
+// programs compiled when there were 11 counters.
+void (skinny_gemm_get_counters)(uint64_t* launches) { skinny_gemm_read_counters(launches, 11); }
 
 void skinny_gemm_reset_counters(void) {
     for (int i = 0; i < SG_NUM_COUNTERS; ++i) g_launches[i].store(0, std::memory_order_relaxed);

@@ -184,3 +184,22 @@ def test_import_and_sizes_without_torchs_gpu_names():
             "print('ok')")
     out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert out.returncode == 0 and out.stdout.strip() == "ok", out.stderr
+
+
+def test_counters_of_a_caller_with_an_older_header():
+    """skinny_gemm_get_counters of a program compiled when there were 11 counters writes 11; the
+    sized form, which the header maps the name to now, writes as many as it is given room for."""
+    lib = ctypes.CDLL(sg.library_path())
+    mark = 0xabadcafe
+    buf = (ctypes.c_uint64 * 20)(*[mark] * 20)
+    lib.skinny_gemm_get_counters(buf)
+    assert list(buf[11:]) == [mark] * 9 and mark not in buf[:11]
+    for n in (0, 3, sg.SG_NUM_COUNTERS, 20):
+        buf = (ctypes.c_uint64 * 20)(*[mark] * 20)
+        lib.skinny_gemm_read_counters(buf, n)
+        kept = min(n, sg.SG_NUM_COUNTERS)
+        assert mark not in buf[:kept] and set(buf[kept:n]) <= {0} and list(buf[n:]) == [mark] * (20 - n)
+    lib.skinny_gemm_read_counters(None, 3)
+    lib.skinny_gemm_read_counters(buf, -1)
+    assert len(sg.skinny_gemm_get_counters()) == sg.SG_NUM_COUNTERS
+    assert sg.skinny_gemm_read_counters(3) == sg.skinny_gemm_get_counters()[:3]
