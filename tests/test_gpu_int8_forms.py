@@ -7,6 +7,7 @@ import torch
 import int8_ref as ref
 import skinny_gemm_projection_amd as sg
 from gpu_common import DEV, announce
+from test_gpu_int8 import check_norm, check_quant, norm_inputs, same
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs an MI355X")]
@@ -73,3 +74,54 @@ def test_norm_with_the_smallest_eps():
     assert torch.equal(codes.cpu(), want)
     s64 = amax.double() * inv / 127.0
     assert ((scales.cpu().double() - s64).abs() <= (rel + 3 * ref.U) * s64).all()
+
+
+# ------------------------------------------------------------------ row kernels of long prompts
+
+# rows of 2056..8192 values take 1024 threads each below 256 rows and 256 threads from there on
+LONG_K = [2056, 4096, 4104, 7168, 8192]
+
+
+@pytest.mark.parametrize("K", LONG_K)
+def test_norm_on_both_sides_of_256_rows(K):
+    announce(f"rmsnorm 255..257 x {K}")
+    x, r, g = norm_inputs(257, K, 20 + K)
+    dx, dr, dg = x.to(DEV), r.to(DEV), g.to(DEV)
+    got = {}
+    for M in (255, 256, 257):
+        h, y = torch.empty_like(dx[:M]), torch.empty_like(dx[:M])
+        codes = torch.full((M + 1, K), 99, dtype=torch.int8, device=DEV)
+        scales = torch.full((M + 1,), -7.0, device=DEV)
+        sg.skinny_rmsnorm(dx[:M], dg, EPS, r=dr[:M], h=h, y_bf16=y, codes=codes[:M], scales=scales[:M])
+        check_norm(x[:M], r[:M], g, EPS, h, y, codes[:M], scales[:M], f"M={M} K={K}")
+        assert (codes[M] == 99).all() and scales[M] == -7.0
+        got[M] = h, codes[:M]
+        hr, yx = dr[:M].clone(), dx[:M].clone()  # h over r, y over x
+        sg.skinny_rmsnorm(yx, dg, EPS, r=hr, h=hr, y_bf16=yx)
+        same(hr, h, "h in place"), same(yx, y, "y in place")
+        y2 = torch.empty_like(y)  # bf16 alone, no residual
+        sg.skinny_rmsnorm(dx[:M], dg, EPS, y_bf16=y2)
+        check_norm(x[:M], None, g, EPS, None, y2, None, None, "bf16 alone")
+    for M in (255, 256):  # a row's h and codes do not depend on the batch
+        same(got[M][0], got[257][0][:M], "h"), same(got[M][1], got[257][1][:M], "codes")
+
+
+@pytest.mark.parametrize("K", LONG_K)
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+def test_quant_on_both_sides_of_256_rows(K, f32, gated):
+    announce(f"quant_int8 255..257 x {K} f32={f32} gated={gated}")
+    x = torch.randn((257, 2 * K if gated else K), generator=torch.Generator().manual_seed(K)) * 2
+    x[3, 5], x[256, K - 1] = float("nan"), float("inf")
+    x[7] = 0
+    x = x if f32 else x.to(BF16)
+    got = {}
+    for M in (255, 256, 257):
+        codes = torch.full((M + 1, K), 99, dtype=torch.int8, device=DEV)
+        scales = torch.full((M + 1,), -7.0, device=DEV)
+        sg.skinny_quant_int8(x[:M].to(DEV), gated, codes[:M], scales[:M])
+        check_quant(x[:M], gated, codes[:M], scales[:M], f"M={M} K={K}")
+        assert (codes[M] == 99).all() and scales[M] == -7.0
+        got[M] = codes[:M], scales[:M]
+    for M in (255, 256):
+        same(got[M][0], got[257][0][:M], "codes"), same(got[M][1], got[257][1][:M], "scales")
