@@ -6,8 +6,10 @@ import torch
 
 import int8_ref as ref
 import skinny_gemm_projection_amd as sg
-from gpu_common import DEV, announce
-from test_gpu_int8 import check_norm, check_quant, norm_inputs, same
+from gpu_common import DEV, announce, counters_delta
+from int8_forms import BLOCKS, PRODUCTS, SPLITS, form
+from test_gpu_int8 import (check_norm, check_quant, mlp_inputs, norm_inputs, parts, product_inputs,
+                           same)
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs an MI355X")]
@@ -125,3 +127,68 @@ def test_quant_on_both_sides_of_256_rows(K, f32, gated):
         got[M] = codes[:M], scales[:M]
     for M in (255, 256):
         same(got[M][0], got[257][0][:M], "codes"), same(got[M][1], got[257][1][:M], "scales")
+
+
+# ------------------------------------------------------------------ forms of the product
+
+
+def check_product(M, N, K, launches):
+    cpu, d = product_inputs(M, N, K, 5)
+    r = torch.randn((M, N), generator=torch.Generator().manual_seed(9)).to(BF16)
+    flat32 = torch.full((M * N + 16,), -7.0, device=DEV)
+    flat16 = torch.full((M * N + 16,), -7.0, device=DEV, dtype=BF16)
+    before = sg.skinny_gemm_get_counters()
+    sg.skinny_gemm_int8(*d, r=r.to(DEV), y_f32=flat32[:M * N].view(M, N), y_bf16=flat16[:M * N].view(M, N))
+    torch.cuda.synchronize()
+    ran = counters_delta(before, sg.skinny_gemm_get_counters())
+    assert (ran[sg.SG_KERNEL_INT8], ran[sg.SG_KERNEL_REDUCE]) == launches
+    want = ref.linear(*cpu, r)
+    for flat, t in ((flat32, torch.float32), (flat16, BF16)):
+        same(flat[:M * N].view(M, N), want.to(t), str(t))
+        assert (flat[M * N:] == -7.0).all(), f"{t}: behind the last element"
+    y, _ = sg.skinny_gemm_int8(*d)
+    same(y, ref.linear(*cpu), "no residual")
+    return cpu, d
+
+
+@pytest.mark.parametrize("M,N,K,kind", PRODUCTS)
+def test_products_of_two_launches(M, N, K, kind):
+    """Whole rounds of the largest tiles, then the other columns in tiles of each smaller size."""
+    announce(f"int8 M={M} N={N} K={K}: {kind}")
+    assert form(M, N, K) == kind
+    check_product(M, N, K, (2, 0))
+
+
+@pytest.mark.parametrize("M,N,K,kind", SPLITS)
+def test_products_split_between_workgroups(M, N, K, kind):
+    """Every tile size with its K split: the workspace is needed, long enough, and not overrun."""
+    announce(f"int8 M={M} N={N} K={K}: {kind}")
+    need = sg.skinny_gemm_int8_workspace(M, N, K)
+    assert form(M, N, K) == kind and need > 0
+    cpu, d = check_product(M, N, K, (1, 1))
+    want = ref.linear(*cpu)
+    for fill in (0, 255):
+        ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device=DEV)
+        y, _ = sg.skinny_gemm_int8(*d, workspace=ws)
+        same(y, want, f"workspace of {fill}")
+        assert (ws[need:] == fill).all()
+    before = sg.skinny_gemm_get_counters()
+    with pytest.raises(sg.SkinnyGemmError) as e:
+        sg.skinny_gemm_int8(*d, workspace=torch.empty(need - 16, dtype=torch.uint8, device=DEV))
+    assert e.value.status == 5
+    assert counters_delta(before, sg.skinny_gemm_get_counters()) == [0] * sg.SG_NUM_COUNTERS
+
+
+@pytest.mark.parametrize("M,H,F,kind", BLOCKS)
+def test_gated_products_of_two_launches(M, H, F, kind):
+    """The MLP block with the gated product in the epilogues of two launches gives the bits of the
+    public calls one after the other, and those are the references'."""
+    announce(f"mlp M={M} H={H} F={F}: {kind}")
+    assert form(M, 2 * F, H) == kind
+    cpu = mlp_inputs(M, H, F, 40 + M)
+    x, r, g, wgu, sgu, wd, sd = [t.to(DEV) for t in cpu]
+    q, sq, u, p, sp, h, want = parts(x, r, g, wgu, sgu, wd, sd)
+    same(sg.skinny_mlp_int8_step(x, g, EPS, wgu, sgu, wd, sd, r=r), want, "step")
+    same(u, ref.linear(q.cpu(), sq.cpu(), cpu[3], cpu[4]), "gate and up")
+    check_quant(u.cpu(), True, p, sp, "gated codes")
+    same(want, ref.linear(p.cpu(), sp.cpu(), cpu[5], cpu[6], h.cpu()).to(BF16), "down")

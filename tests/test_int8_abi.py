@@ -203,3 +203,31 @@ def test_counters_of_a_caller_with_an_older_header():
     lib.skinny_gemm_read_counters(buf, -1)
     assert len(sg.skinny_gemm_get_counters()) == sg.SG_NUM_COUNTERS
     assert sg.skinny_gemm_read_counters(3) == sg.skinny_gemm_get_counters()[:3]
+
+
+def test_every_planned_form_is_in_the_gpu_tests():
+    """The forms that sizes drawn over the whole range plan are those that the GPU tests' sizes
+    reach, and each listed size plans the form it is listed for."""
+    import random
+
+    from int8_forms import BLOCKS, PRODUCTS, SPLITS, form
+    from test_gpu_int8 import GEMM, MLP
+
+    for M, N, K, kind in PRODUCTS + SPLITS:
+        assert form(M, N, K) == kind, (M, N, K)
+    for M, H, F, kind in BLOCKS:
+        assert form(M, 2 * F, H) == kind, (M, H, F)
+    products = {form(*s) for s in GEMM} | {s[3] for s in PRODUCTS + SPLITS}
+    blocks = {form(M, 2 * F, H) for M, H, F in MLP} | {s[3] for s in BLOCKS}
+    rng = random.Random(1)
+
+    def size(lo, hi):
+        return int(round(lo * (hi / lo) ** rng.random()))
+
+    for _ in range(30000):
+        M, N, K = size(1, 9000), size(1, 66000), 16 * size(1, 4096)
+        assert form(M, N, K) in products, (M, N, K, form(M, N, K))
+        H, F = 16 * size(1, 512), 16 * size(1, 1300)
+        kind = form(M, 2 * F, H)
+        if kind[0].isdigit() and "split" not in kind:  # the gated product in the tiles' epilogue
+            assert kind in blocks, (M, H, F, kind)
