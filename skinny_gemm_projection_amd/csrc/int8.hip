@@ -341,13 +341,14 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
         if constexpr (I == 2) return b2;
         if constexpr (I == 3) return b3;
     };
-    __shared__ float sx[BM], sw[BN];
+    __shared__ float sx[BM];
+    __shared__ __attribute__((aligned(16))) float sw[BN];  // read four at a time
     __shared__ uint32_t touched[T::W][kWave];  // where the touching loads land; never read
     // Workgroups reach the 8 XCDs in turn: each XCD takes a run of consecutive
     // tiles, and a run goes down `group` tiles of x before the next tile of W,
     // so the tiles in flight on an XCD share rows of both through its L2.
     const int t = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
-    if ((int)(blockIdx.x / kXcds) >= per_xcd || t >= tiles) return;
+    if (t >= tiles) return;
     // a gated tile is BN / 2 outputs wide: 16 gate rows, then their 16 up rows
     constexpr int BC = OUT == kTileGated ? BN / 2 : BN;
     const int nn = (N + BC - 1) / BC, nm = (M + BM - 1) / BM;
