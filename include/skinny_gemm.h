@@ -306,7 +306,9 @@ size_t skinny_gemm_mxfp4_workspace(int32_t M, int32_t N, int32_t K);
  *
  * Codes of a row v[0..K): amax = max_k |v[k]|, code[k] = v[k] * (127 / amax)
  * rounded once, half to even (the quotient in fp32), scale = amax / 127 (so v is
- * about code * scale; codes lie in [-127, 127]).  A row of zeros has codes 0 and scale 0.  A row
+ * about code * scale; codes lie in [-127, 127]).  Where v * 127 / amax is halfway
+ * between two codes, the rounding of the quotient decides which of the two, both
+ * as near, is taken.  A row of zeros has codes 0 and scale 0.  A row
  * that holds a NaN or an infinity (or whose fp32 intermediates overflow) has
  * codes 0 and scale NaN, so everything computed from it is NaN.
  * Rows never depend on each other, and repeated calls give identical bits.  A
@@ -315,7 +317,7 @@ size_t skinny_gemm_mxfp4_workspace(int32_t M, int32_t N, int32_t K);
  * sizes; all else is the same for a row in any batch. */
 #define SG_INT8_MAX_M (1 << 20)
 #define SG_INT8_MAX_K 131056 /* 2^14 * K < 2^31: every sum of products is exact */
-#define SG_ROW_MAX_K 65536   /* a row is held in the registers of one workgroup */
+#define SG_ROW_MAX_K 65536   /* one workgroup holds a row */
 
 /* Root-mean-square norm with the residual addition, and int8 output:
  *   s = x + r (fp32; r NULL: s = x);  h = bf16(s);

@@ -12,16 +12,17 @@
 // Two kinds of kernel share the batch range:
 //  * team kernels (up to 64 rows): a workgroup owns 16 or 32 rows of W and all
 //    of K, its waves take windows of K in turn and add their sums in LDS.  Bound
-//    by the weight stream from HBM and, from about 16 rows, by the x rows that
-//    every workgroup reads from L2.  2 x 8192 x 7168 takes 10.9 us (5.4 TB/s; a
-//    kernel that only reads W 9.5), 16 x 8192 x 7168 11.1, 4 x 36864 x 7168 40.5
-//    (6.5 TB/s).
+//    by the weight stream from HBM, as far as the waits noted at the kernel let
+//    it run, and, from about 16 rows, by the x rows that every workgroup reads
+//    from L2.  2 x 8192 x 7168 takes 11.2 us (5.3 TB/s; a kernel that only reads
+//    W 9.5), 16 x 7168 x 8192 with the residual 11.5, 4 x 36864 x 7168 40.7 (6.5
+//    TB/s).
 //  * int8_tile_kernel (beyond): a workgroup owns BM rows of x and BN rows of W,
 //    both requested a few stages ahead; K may be split between workgroups, the
 //    int32 partial tiles then go through the workspace to int8_reduce_kernel.
 //    8192 x 8192 x 7168 takes 336 us (2.87 POP/s) on inputs that stay in the
-//    caches and 360 on changing ones; all-zero codes take 271, so the rest is
-//    the clock that the chip's power allows: the matrix cores are busy 70 % of
+//    caches and 354 to 388 on changing ones; all-zero codes take 271, so the rest
+//    is the clock that the chip's power allows: the matrix cores are busy 70 % of
 //    the cycles at about 1.8 GHz.
 // All of them bring codes to LDS with loads that write it directly, 128-byte
 // lines whole.
@@ -142,8 +143,13 @@ __device__ __forceinline__ void finish_team(const uint4* sums, int stride, int M
 }
 
 // S waves share 16 * RT rows of W and all of x; wave s takes the 128-code
-// windows s, s + S, ... of K, D of them in flight, W and x both in LDS slots of
-// the wave's own: no barrier until the sums meet.  A load instruction covers 8
+// windows s, s + S, ... of K through D LDS slots of its own, W and x both: no
+// barrier until the sums meet.  A slot is refilled as soon as it has been read,
+// but only while there is more, and where those two paths meet the compiler
+// waits for the stricter: before a slot is read a wave waits for every load it
+// has out, the refill just requested among them (D = 2; D = 4: all, then all but
+// 2, 1 and 0 slots' worth).  With two slots one window a wave is really in
+// flight, and what overlaps is the waves of a compute unit.  A load instruction covers 8
 // rows x 128 bytes, whole lines: with 64 bytes of 16 rows, the layout of the
 // operand registers, reading W alone took 15 to 25 % longer (7168 x 8192 13.2
 // against 10.7 us), and x came from L2 at 30 against 43 bytes a clock.  The
@@ -225,9 +231,10 @@ __global__ __launch_bounds__(S* kWave) void int8_team_kernel(const int8_t* __res
 
 // The same for a few rows of x and very wide W (many workgroups a compute
 // unit): x goes straight to the operand registers, which leaves the LDS to W,
-// in 256-code windows, and twice as many workgroups resident.  4 x 36864 x 7168
-// takes 40.0 us against 44.1 with x in LDS, 5 x 7820 x 3696 7.6 against 8.7; at
-// 8192 x 7168 the other form is as fast, at 4096 rows of W faster.
+// in 256-code windows, and twice as many workgroups resident.  (The waits before
+// a slot is read cover W of the refill just requested here too.)  1 x 36864 x
+// 7168 takes 43.0 us against 45.9 with x in LDS, 1 x 12304 x 2064 8.8 against
+// 10.7; at 4096 x 7168 the other form is faster, 8.6 against 9.3.
 template <int S>
 __global__ __launch_bounds__(S* kWave) void int8_wide_kernel(const int8_t* __restrict__ xq,
                                                              const int8_t* __restrict__ wq, int M,
@@ -399,7 +406,9 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void int8_tile_kern
     // miss to HBM takes under load.  So every wave also reads one word of some
     // lines of the stage kAhead ahead, which brings them to L2: the workgroups
     // an XCD runs at once share rows (kShareW tiles of x along a tile of W,
-    // kShareX the other way) and touch one part each.  On inputs larger than the
+    // kShareX the other way) and touch one part each; where fewer tiles share
+    // (the last of 6 tiles of x stand in a group of 2), the other parts are not
+    // touched.  On inputs larger than the
     // caches 8192 x 8192 x 7168 takes 359 against 383 us without, 1536 x 7168 x
     // 18432 183 against 219; with three or four buffers it cost 5 to 10 %.
     constexpr bool kTouch = NB == 2;
@@ -659,8 +668,14 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // per KB of W and 0.012 (0.016 past 48 rows) per KB of x that a compute unit
 // takes in.  Tiles: 3 us, then rounds of workgroups at the measured cost per
 // code, but no faster than W comes from HBM; a split adds the reduction's
-// launch and its traffic.  Over 38 shapes of 1 to 4096 rows the choice was
-// within 3 % of the fastest variant on average.
+// launch and its traffic.  Against every other form at 100 sizes drawn from 1 to
+// 4096 rows, 16 to 40000 channels and 64 to 18432 codes the choice takes 4 %
+// longer than the fastest on average, and by more than a tenth for 15.  Those
+// are wide products of 10 to 30 rows, where the team estimate has no rounds and
+// too little for x (13 x 28653 x 3488 27.6 us, 22.0 in tiles; 11 x 35161 x 528
+// 13.5, 8.4 with 16 rows of W a workgroup), few rows and short K on the wide
+// kernel (7 x 15100 x 112 4.7, 3.6 in tiles), and sizes just past a round of
+// tiles (1177 x 2411 x 14672 100.8, 73.6 in large tiles split four ways).
 Int8Plan int8_plan(int M, int N, int K) {
     Int8Plan best{};
     double least = 1e30;
@@ -681,6 +696,19 @@ Int8Plan int8_plan(int M, int N, int K) {
                                 rt == 1 && M <= 16 && wgs <= kCus && K >= 4096 ? 4 : 2, 0, 1, K, 0, 0, 0};
             }
         }
+        // The wide kernel against the team kernel of 16 and 32 rows, M = 1 / 8:
+        //   6160 x 2064     6.1 / 6.5 us   against  6.4 / 6.9 and  6.5 / 6.8
+        //   12304 x 2064    8.8 / 9.5              10.7 / 11.4    11.2 / 11.4
+        //   8208 x 4096     8.6 / 9.5               9.4 / 9.6     10.1 / 10.1
+        //   16400 x 7168   22.2 / 23.7             23.6 / 24.6    24.9 / 25.1
+        //   36864 x 7168   43.0 / 45.7             45.9 / 49.0    47.3 / 48.0
+        // and outside the rule:
+        //   4096 x 4096     5.7 / 6.0               5.6 / 5.6      6.1 / 6.8
+        //   6160 x 7168    10.5 / 11.9             10.4 / 11.4    10.4 / 10.6
+        // It is not the fastest at 6160 x 4096 with 8 rows (8.2 against 7.1) and
+        // would be between 8208 and 16400 rows of W past K = 4096 (12304 x 7168
+        // 18.2 / 19.5 against 19.8 / 20.4 as planned).  The estimate that the
+        // tiles below are held against stays the team kernel's.
         const int64_t wgs = ceil_div(N, 16);
         if (M <= 8 && (wgs > 4 * kCus || (wgs > 1.5 * kCus && K <= 4096)))
             best.kind = Int8Plan::kWide;

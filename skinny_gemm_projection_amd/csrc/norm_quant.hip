@@ -13,13 +13,18 @@
 //
 // A row stays in the registers of one workgroup (each thread holds P pieces of
 // 8 values), so every value is read once and written once and the two row
-// statistics cost one exchange through LDS.
+// statistics cost one exchange through LDS.  Norms of rows past 32768 values are
+// the exception: P = 8 spills 25 registers a thread to scratch.  1024 x 65536
+// with residual and int8 output takes 116 us, 2048 x 32768, as many bytes, 98;
+// one row of 65536 10.0, of 32768 4.9.
 //
 // Many rows are bound by HBM: 8191 x 7168 with residual, bf16 and int8 output
-// (528 MB) takes 92 us, 5.7 TB/s; 5003 x 8192 bf16 codes (123 MB) 22.9 us, 5.4
-// TB/s; a copy reaches 5.1.  One row takes 2.8 us, a launch and two memory
-// latencies.  64 gated fp32 rows of 18432 take 6.9 us: 64 workgroups, more than
-// half of it in the exponential and the quotient of each value.
+// (528 MB) takes 92 us, 5.7 TB/s; without the bf16 output 74 (5.5); bf16 output
+// alone without a residual 44 (5.4); 5003 x 8192 bf16 codes (123 MB) 22.7 us, 5.4
+// TB/s; a copy reaches 4.8 to 5.1.  One row takes 2.8 us, a launch and two memory
+// latencies.  Gated rows are bound by the exponential and the quotient of each
+// value too: 64 x 18432 from fp32 6.9 us (64 workgroups), from bf16 7.1; 4096 x
+// 8192 from bf16 (168 MB) 35.3, 4.8 TB/s.
 #include <math.h>
 
 #include <type_traits>
