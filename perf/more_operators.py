@@ -217,6 +217,7 @@ def _quant(v):
     t[:, :K] = v
     t = t.view(M, kb, B)
     man, ex = torch.frexp(t.abs().amax(dim=2))  # man in [0.5, 1); 448 = 0.875 * 2^9
+    ex = torch.where(man > 0, ex, torch.full_like(ex, -126))  # a block of zeros: the least scale
     unit = torch.ldexp(torch.ones_like(man), (ex - 9 + (man > 0.875).int()).clamp_min(-126))
     codes = (t / unit[:, :, None]).to(E4M3)  # the quotient is exact
     return codes.view(M, kb * B)[:, :K].contiguous(), unit.t().contiguous()
