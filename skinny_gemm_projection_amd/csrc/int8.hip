@@ -28,33 +28,19 @@
 // lines whole.
 #include <type_traits>
 
-#include "int8_device.h"
 #include "launch.h"
+#include "tile_device.h"
 
 namespace sg {
 
 namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void_t;
-
-// A buffer offset that reads zeros, also after a row offset is added: buffers
-// here end below 2^31 and rows of one tile span less than 2^27 bytes.
-constexpr uint32_t kPastEnd = 1u << 31;
 
 __device__ __forceinline__ i32x4_t mfma16(const uint4 w, const uint4 x, i32x4_t acc) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, w),
                                                  __builtin_bit_cast(i32x4_t, x), acc, 0, 0, 0);
 }
-
-// 64 lanes x 16 bytes from the buffer (each lane its own offset) to 1 KB of LDS.
-template <int POLICY>
-__device__ __forceinline__ void load_to_lds(rsrc_t r, uint4* lds, uint32_t offset) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds, 16, (int)offset, 0, 0, POLICY);
-}
-
-// Before a wave refills an LDS slot of its own: its reads of the slot are done.
-__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // y of four neighbouring outputs: one rounding for the conversion and each product
 __device__ __forceinline__ void scale4(const i32x4_t acc, const float4 ws, float xs, float (&y)[4]) {
@@ -63,41 +49,6 @@ __device__ __forceinline__ void scale4(const i32x4_t acc, const float4 ws, float
     y[1] = (float)acc[1] * ws.y * xs;
     y[2] = (float)acc[2] * ws.z * xs;
     y[3] = (float)acc[3] * ws.w * xs;
-}
-
-// Outputs y[m][n .. n+4) with the residual, one access each way also where rows
-// of y are not 4-element aligned: global memory takes any alignment.  (333 x 5001
-// x 2064: 10.9 us, as for 5008 columns; four scalar stores a lane 15.5, rows
-// turned in LDS and stored an element a lane 12.3.)
-__device__ __forceinline__ void finish4(const Int8Epilogue& ep, int N, int m, int n, float (&y)[4]) {
-    const int64_t at = (int64_t)m * ep.ld + n;
-    if (n + 4 <= N) {
-        if (ep.r) {
-            uint2 r;
-            __builtin_memcpy(&r, ep.r + at, 8);
-            y[0] = as_f(r.x << 16) + y[0];
-            y[1] = as_f(r.x & 0xffff0000u) + y[1];
-            y[2] = as_f(r.y << 16) + y[2];
-            y[3] = as_f(r.y & 0xffff0000u) + y[3];
-        }
-        if (ep.y_f32) {
-            const float4 v = make_float4(y[0], y[1], y[2], y[3]);
-            __builtin_memcpy(ep.y_f32 + at, &v, 16);
-        }
-        if (ep.y_bf16) {
-            const uint2 v = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-            __builtin_memcpy(ep.y_bf16 + at, &v, 8);
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            if (n + v >= N) break;
-            float o = y[v];
-            if (ep.r) o = bf16_to_f32(ep.r[at + v]) + o;
-            if (ep.y_f32) ep.y_f32[at + v] = o;
-            if (ep.y_bf16) ep.y_bf16[at + v] = f32_to_bf16(o);
-        }
-    }
 }
 
 // scales of channels n .. n+4 (zeros past N)
@@ -284,12 +235,6 @@ __global__ __launch_bounds__(S* kWave) void int8_wide_kernel(const int8_t* __res
 
 // ---------------------------------------------------------------- tile kernel
 
-template <int N>
-__device__ __forceinline__ void wait_and_barrier() {
-    // at most N loads of this wave outstanding, its LDS reads done, then all waves
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
-}
-
 // Schedules one step: FM + FN LDS reads (the next step's operands) and LOADS
 // loads of a later stage, spread over the FM * FN products of this step.
 template <int I, int FM, int FN, int LOADS>
@@ -301,14 +246,6 @@ __device__ __forceinline__ void interleave() {
         __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);  // LDS reads
         __builtin_amdgcn_sched_group_barrier(0x8, FN, 0);        // matrix instructions
         interleave<I + 1, FM, FN, LOADS>();
-    }
-}
-
-template <int I, int END, class F>
-__device__ __forceinline__ void unrolled(F f) {
-    if constexpr (I < END) {
-        f(std::integral_constant<int, I>{});
-        unrolled<I + 1, END>(f);
     }
 }
 
