@@ -22,7 +22,8 @@ from ._lib import (KERNEL_NAMES, SG_KERNEL_GEMV, SG_KERNEL_GROUPED, SG_KERNEL_MO
                    SG_KERNEL_ROUTER_TOPK,
                    SG_KERNEL_SPLITK_MFMA, SG_KERNEL_SPLITK_VALU, SG_NOALLOC_MAX_WORKSPACE,
                    SG_KERNEL_INT8, SG_KERNEL_QUANT_INT8, SG_KERNEL_RMSNORM,
-                   SG_NUM_COUNTERS, SgMlpInt8Step, SgMoeStep,
+                   SG_KERNEL_FP8_BLOCK, SG_KERNEL_MOE_ROWS, SG_KERNEL_MOE_SORT, SG_KERNEL_QUANT_FP8,
+                   SG_NUM_COUNTERS, SgMlpInt8Step, SgMoeFp8Step, SgMoeStep,
                    SgPlan, SkinnyGemmError)
 
 __all__ = [
@@ -35,6 +36,11 @@ __all__ = [
     "skinny_rmsnorm", "skinny_quant_int8", "skinny_gemm_int8", "skinny_gemm_int8_workspace",
     "skinny_mlp_int8_step", "skinny_mlp_int8_step_workspace",
     "SG_KERNEL_INT8", "SG_KERNEL_RMSNORM", "SG_KERNEL_QUANT_INT8",
+    "skinny_quant_fp8", "skinny_gemm_fp8_block", "skinny_gemm_fp8_block_workspace",
+    "skinny_moe_sort", "skinny_moe_sort_workspace", "skinny_moe_gather", "skinny_moe_combine",
+    "skinny_moe_combine_grad", "grouped_skinny_gemm_fp8", "skinny_moe_fp8_step",
+    "skinny_moe_fp8_step_workspace",
+    "SG_KERNEL_FP8_BLOCK", "SG_KERNEL_QUANT_FP8", "SG_KERNEL_MOE_SORT", "SG_KERNEL_MOE_ROWS",
     "skinny_gemm_status_str", "skinny_gemm_read_counters", "skinny_gemm_get_counters",
     "skinny_gemm_reset_counters",
     "SgPlan", "SkinnyGemmError", "KERNEL_NAMES", "SG_KERNEL_NONE", "SG_KERNEL_GEMV",
@@ -377,13 +383,20 @@ def _rows(x, name, dtypes):
     return M, K, x.device, x.data_ptr()
 
 
+def _as_stream(stream, dev):
+    """The torch stream a call runs on: dev's current one by default."""
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return stream
+
+
 def _new(shape, dtype, dev, stream):
     """A tensor the work on `stream` may use at once: taken from that stream's memory."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_as_stream(stream, dev)):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
@@ -522,6 +535,251 @@ def skinny_mlp_int8_step(x: torch.Tensor, g: torch.Tensor, eps: float, W_gate_up
         _arg(W_down, i8, (H, F), "W_down", dev), _arg(down_scales, f32, (H,), "down_scales", dev),
         _arg(out, bf16, (M, H), "out", dev), M, H, F, eps)
     _run_on(dev, stream, _c().skinny_mlp_int8_step, ctypes.byref(step), ws_ptr, ws_bytes)
+    return out
+
+
+# ---- block-scaled FP8 rows, and tokens sorted by expert and back ----
+
+
+def _blocks(n):
+    return (n + 127) >> 7
+
+
+def skinny_quant_fp8(x: torch.Tensor, gated: bool = False, codes=None, scales=None, stream=None):
+    """e4m3 codes uint8 [M, K] and scales float32 [ceil(K/128), M] of rows of x (bf16 or
+    float32): of x [M, K] itself, or with gated of silu(x[:, :K]) * x[:, K:] for x [M, 2K].  Each
+    row's block of 128 columns has the least power of two as its scale that brings it to at most
+    448.  Returns (codes, scales)."""
+    M, K, dev, px = _rows(x, "x", (torch.bfloat16, torch.float32))
+    if gated:
+        if K % 2:
+            raise ValueError(f"x: gated rows hold gate and up halves, got {K} columns")
+        K //= 2
+    if codes is None:
+        codes = _new((M, K), torch.uint8, dev, stream)
+    if scales is None:
+        scales = _new((_blocks(K), M), torch.float32, dev, stream)
+    f32 = x.dtype is torch.float32
+    _run_on(dev, stream, _c().skinny_quant_fp8, M, K, None if f32 else px, px if f32 else None,
+            1 if gated else 0, _arg(codes, torch.uint8, (M, K), "codes", dev),
+            _arg(scales, torch.float32, (_blocks(K), M), "scales", dev))
+    return codes, scales
+
+
+def skinny_gemm_fp8_block_workspace(M: int, N: int, K: int, with_f32: bool) -> int:
+    """Workspace bytes skinny_gemm_fp8_block needs for an M x N x K product (0 when none);
+    with_f32: whether y_f32 is given."""
+    return int(_c().skinny_gemm_fp8_block_workspace(M, N, K, 1 if with_f32 else 0))
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp8_block_workspace(M, N, K, with_f32):
+    return _c().skinny_gemm_fp8_block_workspace(M, N, K, with_f32)
+
+
+def skinny_gemm_fp8_block(x_codes: torch.Tensor, x_scales: torch.Tensor, W_codes: torch.Tensor,
+                          W_scales: torch.Tensor, y_f32=None, y_bf16=None, r=None, workspace=None,
+                          stream=None):
+    """y = x W^T for e4m3 codes on both sides (uint8): x_codes [M, K] with scales float32
+    [ceil(K/128), M] (as skinny_quant_fp8 makes them), W_codes [N, K] with scales float32
+    [ceil(N/128), ceil(K/128)]; any M up to 2^20.  Writes y_f32 and/or y_bf16 [M, N]; with r (bf16
+    [M, N]) the fused residual y = r + product (y_bf16 may be r).  Allocates y_f32 when no output
+    is given, and the workspace when one is needed and none is given; returns the outputs.
+    (y_bf16 alone, past 64 rows, takes the FP8 matrix instruction: see the header on its sums.)"""
+    u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
+    M, K, dev, px = _rows(x_codes, "x_codes", (u8,))
+    N, _, _, pw = _rows(W_codes, "W_codes", (u8,))
+    if W_codes.shape[1] != K or W_codes.get_device() != dev.index:
+        _arg(W_codes, u8, (N, K), "W_codes", dev)  # raises
+    mn = (M, N)
+    if y_f32 is None and y_bf16 is None:
+        y_f32 = _new(mn, f32, dev, stream)
+    ws, ws_ptr, ws_bytes = _ws_arg(workspace, _fp8_block_workspace(M, N, K, 0 if y_f32 is None else 1),
+                                   dev, stream)
+    _run_on(dev, stream, _c().skinny_gemm_fp8_block, M, N, K, px,
+            _arg(x_scales, f32, (_blocks(K), M), "x_scales", dev), pw,
+            _arg(W_scales, f32, (_blocks(N), _blocks(K)), "W_scales", dev),
+            None if r is None else _arg(r, bf16, mn, "r", dev),
+            None if y_f32 is None else _arg(y_f32, f32, mn, "y_f32", dev),
+            None if y_bf16 is None else _arg(y_bf16, bf16, mn, "y_bf16", dev), ws_ptr, ws_bytes)
+    return y_f32, y_bf16
+
+
+def skinny_moe_sort_workspace(T: int, topk: int, E: int) -> int:
+    """Workspace bytes skinny_moe_sort needs (0 when none)."""
+    return int(_c().skinny_moe_sort_workspace(T, topk, E))
+
+
+def skinny_moe_sort(topk_ids: torch.Tensor, E: int, expert_offsets=None, sorted_pairs=None,
+                    positions=None, workspace=None, stream=None):
+    """The pairs p = t * topk + j of topk_ids (int32 [T, topk]) sorted by expert, ascending in p
+    inside an expert; ids outside [0, E) are left out.  Returns int32 (expert_offsets [E + 1],
+    sorted_pairs [T * topk] with -1 behind the last, positions [T, topk]: a pair's place, -1 if
+    left out), each allocated when not given."""
+    T, topk, dev, pi = _rows(topk_ids, "topk_ids", (torch.int32,))
+    i32 = torch.int32
+    if not 0 < E <= 0x7fffffff:
+        raise ValueError(f"E: expected a positive number of experts, got {E}")
+    if expert_offsets is None:
+        expert_offsets = _new((E + 1,), i32, dev, stream)
+    if sorted_pairs is None:
+        sorted_pairs = _new((T * topk,), i32, dev, stream)
+    if positions is None:
+        positions = _new((T, topk), i32, dev, stream)
+    ws, ws_ptr, ws_bytes = _ws_arg(workspace, _c().skinny_moe_sort_workspace(T, topk, E), dev, stream)
+    _run_on(dev, stream, _c().skinny_moe_sort, T, topk, E, pi,
+            _arg(expert_offsets, i32, (E + 1,), "expert_offsets", dev),
+            _arg(sorted_pairs, i32, (T * topk,), "sorted_pairs", dev),
+            _arg(positions, i32, (T, topk), "positions", dev), ws_ptr, ws_bytes)
+    return expert_offsets, sorted_pairs, positions
+
+
+def _table_of(positions):
+    T, topk, dev, pp = _rows(positions, "positions", (torch.int32,))
+    return T, topk, dev, pp
+
+
+_ROW_TYPES = (torch.bfloat16, torch.float32)
+
+
+def skinny_moe_gather(x: torch.Tensor, positions: torch.Tensor, out=None, stream=None):
+    """out[positions[t, j]] = x[t]: token rows (bf16 or float32 [T, K]) laid out by expert, [T *
+    topk, K].  Rows that no position names are left as they were (zeros in an out allocated
+    here).  Its gradient is skinny_moe_combine without weights.  Returns out."""
+    T, topk, dev, pp = _table_of(positions)
+    n, K, _, px = _rows(x, "x", _ROW_TYPES)
+    if n != T or x.get_device() != dev.index:
+        _arg(x, x.dtype, (T, K), "x", dev)  # raises
+    if out is None:
+        out = _new((T * topk, K), x.dtype, dev, stream)
+        with torch.cuda.stream(_as_stream(stream, dev)):
+            out.zero_()
+    _run_on(dev, stream, _c().skinny_moe_gather, T, topk, K, px, 1 if x.dtype is torch.float32 else 0,
+            pp, _arg(out, x.dtype, (T * topk, K), "out", dev))
+    return out
+
+
+def skinny_moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights, r=None, out=None,
+                       stream=None):
+    """out[t] = (r[t] +) sum_j weights[t, j] * rows[positions[t, j]]: expert outputs (bf16 or
+    float32 [T * topk, K]) back to their tokens, left-out pairs skipped; weights float32 [T, topk]
+    or None (all 1).  r and out [T, K] of the rows' type, out may be r; fp32 sums, one rounding.
+    Returns out."""
+    T, topk, dev, pp = _table_of(positions)
+    n, K, _, pr = _rows(rows, "rows", _ROW_TYPES)
+    if n != T * topk or rows.get_device() != dev.index:
+        _arg(rows, rows.dtype, (T * topk, K), "rows", dev)  # raises
+    if out is None:
+        out = _new((T, K), rows.dtype, dev, stream)
+    _run_on(dev, stream, _c().skinny_moe_combine, T, topk, K, pr,
+            1 if rows.dtype is torch.float32 else 0, pp,
+            None if weights is None else _arg(weights, torch.float32, (T, topk), "weights", dev),
+            None if r is None else _arg(r, rows.dtype, (T, K), "r", dev),
+            _arg(out, rows.dtype, (T, K), "out", dev))
+    return out
+
+
+def skinny_moe_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, positions: torch.Tensor,
+                            weights: torch.Tensor, d_rows=None, d_weights=None, stream=None):
+    """Gradient of skinny_moe_combine for d_out [T, K]: d_rows[positions[t, j]] = weights[t, j] *
+    d_out[t] (bf16 or float32 [T * topk, K] like rows; may be rows itself; rows that no position
+    names are left as they were, zeros in a d_rows allocated here) and d_weights[t, j] = <d_out[t],
+    rows[positions[t, j]]> (float32 [T, topk], 0 where left out).  Returns (d_rows, d_weights)."""
+    T, topk, dev, pp = _table_of(positions)
+    n, K, _, pr = _rows(rows, "rows", _ROW_TYPES)
+    if n != T * topk or rows.get_device() != dev.index:
+        _arg(rows, rows.dtype, (T * topk, K), "rows", dev)  # raises
+    if d_rows is None:
+        d_rows = _new((T * topk, K), rows.dtype, dev, stream)
+        with torch.cuda.stream(_as_stream(stream, dev)):
+            d_rows.zero_()
+    if d_weights is None:
+        d_weights = _new((T, topk), torch.float32, dev, stream)
+    _run_on(dev, stream, _c().skinny_moe_combine_grad, T, topk, K,
+            _arg(d_out, rows.dtype, (T, K), "d_out", dev), pr,
+            1 if rows.dtype is torch.float32 else 0, pp,
+            _arg(weights, torch.float32, (T, topk), "weights", dev),
+            _arg(d_rows, rows.dtype, (T * topk, K), "d_rows", dev),
+            _arg(d_weights, torch.float32, (T, topk), "d_weights", dev))
+    return d_rows, d_weights
+
+
+def _experts(W, name, dev):
+    """(E, N, K, pointer) of contiguous uint8 expert weights on dev."""
+    _ptr(W, torch.uint8, name, dev)
+    if W.dim() != 3 or max(W.shape) > 0x7fffffff:
+        raise ValueError(f"{name}: expected [E, N, K], got shape {tuple(W.shape)}")
+    return (*W.shape, W.data_ptr())
+
+
+def grouped_skinny_gemm_fp8(x_codes: torch.Tensor, x_scales: torch.Tensor, W_codes: torch.Tensor,
+                            W_scales: torch.Tensor, expert_offsets: torch.Tensor, sorted_pairs=None,
+                            topk: int = 1, y_f32=None, y_bf16=None, stream=None):
+    """y[i] = x_i W[e]^T for the rows expert_offsets[e] <= i < expert_offsets[e + 1] of every
+    expert e: W_codes uint8 [E, N, K] with scales float32 [E, ceil(N/128), ceil(K/128)].  x_i is
+    row i of x_codes [rows, K], or with sorted_pairs (int32 [rows], skinny_moe_sort's) row
+    sorted_pairs[i] // topk of x_codes [T, K]; x_scales [ceil(K/128), rows of x_codes].  Writes
+    y_f32 and/or y_bf16 [rows, N]; rows behind the last segment are left as they were (zeros in a
+    y_f32 allocated here, which happens when no output is given).  Returns the outputs."""
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    X, K, dev, px = _rows(x_codes, "x_codes", (u8,))
+    E, N, K2, pw = _experts(W_codes, "W_codes", dev)
+    if K2 != K:
+        raise ValueError(f"W_codes: {K2} columns, x_codes has {K}")
+    if sorted_pairs is None:
+        rows = X
+    else:
+        if not isinstance(sorted_pairs, torch.Tensor):
+            raise TypeError(f"sorted_pairs: expected a torch.Tensor, got {type(sorted_pairs).__name__}")
+        rows = sorted_pairs.numel()
+    if y_f32 is None and y_bf16 is None:
+        y_f32 = _new((rows, N), f32, dev, stream)
+        with torch.cuda.stream(_as_stream(stream, dev)):
+            y_f32.zero_()
+    _run_on(dev, stream, _c().grouped_skinny_gemm_fp8, rows, X, E, N, K, px,
+            _arg(x_scales, f32, (_blocks(K), X), "x_scales", dev), pw,
+            _arg(W_scales, f32, (E, _blocks(N), _blocks(K)), "W_scales", dev),
+            _arg(expert_offsets, i32, (E + 1,), "expert_offsets", dev),
+            None if sorted_pairs is None else _arg(sorted_pairs, i32, (rows,), "sorted_pairs", dev),
+            topk, None if y_f32 is None else _arg(y_f32, f32, (rows, N), "y_f32", dev),
+            None if y_bf16 is None else _arg(y_bf16, torch.bfloat16, (rows, N), "y_bf16", dev))
+    return y_f32, y_bf16
+
+
+def skinny_moe_fp8_step_workspace(T: int, topk: int, E: int, H: int, F: int) -> int:
+    """Workspace bytes skinny_moe_fp8_step needs (0 if the sizes are rejected)."""
+    return int(_c().skinny_moe_fp8_step_workspace(T, topk, E, H, F))
+
+
+def skinny_moe_fp8_step(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                        W_gate_up: torch.Tensor, gate_up_scales: torch.Tensor,
+                        W_down: torch.Tensor, down_scales: torch.Tensor, r=None, out=None,
+                        workspace=None, stream=None):
+    """The routed experts of any number of tokens, with block-scaled FP8 weights: out[t] = (r[t] +)
+    sum_j topk_weights[t, j] * down_e(swiglu(gate_up_e(x[t]))) for e = topk_ids[t, j], x and the
+    gated product quantised by skinny_quant_fp8; ids outside [0, E) are left out.  x, r [T, H] bf16,
+    topk_ids int32 and topk_weights float32 [T, topk], W_gate_up uint8 [E, 2F, H] (gate rows, then
+    up rows) and W_down uint8 [E, H, F] with float32 scales per 128 x 128 block.  out bf16 [T, H]
+    (may be x or r itself; allocated when not given).  Returns out."""
+    T, H, dev, px = _rows(x, "x", (torch.bfloat16,))
+    topk = _rows(topk_ids, "topk_ids", (torch.int32,))[1]
+    E, _, F, pd = _experts(W_down, "W_down", dev)
+    if out is None:
+        out = _new((T, H), torch.bfloat16, dev, stream)
+    ws, ws_ptr, ws_bytes = _ws_arg(workspace, _c().skinny_moe_fp8_step_workspace(T, topk, E, H, F), dev,
+                                   stream)
+    u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
+    hb, fb = _blocks(H), _blocks(F)
+    step = SgMoeFp8Step(
+        px, _arg(topk_ids, torch.int32, (T, topk), "topk_ids", dev),
+        _arg(topk_weights, f32, (T, topk), "topk_weights", dev),
+        _arg(W_gate_up, u8, (E, 2 * F, H), "W_gate_up", dev),
+        _arg(gate_up_scales, f32, (E, _blocks(2 * F), hb), "gate_up_scales", dev),
+        _arg(W_down, u8, (E, H, F), "W_down", dev),
+        _arg(down_scales, f32, (E, hb, fb), "down_scales", dev),
+        None if r is None else _arg(r, bf16, (T, H), "r", dev),
+        _arg(out, bf16, (T, H), "out", dev), T, topk, E, H, F)
+    _run_on(dev, stream, _c().skinny_moe_fp8_step, ctypes.byref(step), ws_ptr, ws_bytes)
     return out
 
 

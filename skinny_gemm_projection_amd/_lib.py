@@ -29,10 +29,15 @@ SG_KERNEL_FP8 = 10
 SG_KERNEL_INT8 = 11
 SG_KERNEL_RMSNORM = 12
 SG_KERNEL_QUANT_INT8 = 13
-SG_NUM_COUNTERS = 14
+SG_KERNEL_FP8_BLOCK = 14
+SG_KERNEL_QUANT_FP8 = 15
+SG_KERNEL_MOE_SORT = 16
+SG_KERNEL_MOE_ROWS = 17
+SG_NUM_COUNTERS = 18
 KERNEL_NAMES = {0: "none", 1: "gemv", 2: "splitk_valu", 3: "splitk_mfma", 4: "reduce",
                 5: "moe_table", 6: "grouped", 7: "prefetch", 8: "router_topk", 9: "mxfp4",
-                10: "fp8", 11: "int8", 12: "rmsnorm", 13: "quant_int8"}
+                10: "fp8", 11: "int8", 12: "rmsnorm", 13: "quant_int8", 14: "fp8_block", 15: "quant_fp8",
+                16: "moe_sort", 17: "moe_rows"}
 
 
 class SgPlan(ctypes.Structure):
@@ -72,6 +77,16 @@ class SgMlpInt8Step(ctypes.Structure):
                 ("out", ctypes.c_void_p),
                 ("M", ctypes.c_int32), ("H", ctypes.c_int32), ("F", ctypes.c_int32),
                 ("eps", ctypes.c_float)]
+
+
+class SgMoeFp8Step(ctypes.Structure):
+    """Mirror of sg_moe_fp8_step."""
+    _fields_ = [("x", ctypes.c_void_p), ("topk_ids", ctypes.c_void_p),
+                ("topk_weights", ctypes.c_void_p), ("W_gate_up", ctypes.c_void_p),
+                ("gate_up_scales", ctypes.c_void_p), ("W_down", ctypes.c_void_p),
+                ("down_scales", ctypes.c_void_p), ("r", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("T", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("H", ctypes.c_int32), ("F", ctypes.c_int32)]
 
 
 SG_MOE_STEP_FUSED_SHARED = 1
@@ -125,6 +140,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         getattr(lib, name).argtypes = [i32, i32, i32]
         getattr(lib, name).restype = sz
     lib.skinny_mlp_int8_step.argtypes = [ctypes.POINTER(SgMlpInt8Step), p, sz, p]
+    lib.skinny_quant_fp8.argtypes = [i32, i32, p, p, i32, p, p, p]
+    lib.skinny_gemm_fp8_block.argtypes = [i32, i32, i32, p, p, p, p, p, p, p, p, sz, p]
+    lib.skinny_gemm_fp8_block_workspace.argtypes = [i32, i32, i32, i32]
+    lib.skinny_moe_sort.argtypes = [i32, i32, i32, p, p, p, p, p, sz, p]
+    lib.skinny_moe_sort_workspace.argtypes = [i32, i32, i32]
+    lib.skinny_moe_gather.argtypes = [i32, i32, i32, p, i32, p, p, p]
+    lib.skinny_moe_combine.argtypes = [i32, i32, i32, p, i32, p, p, p, p, p]
+    lib.skinny_moe_combine_grad.argtypes = [i32, i32, i32, p, p, i32, p, p, p, p, p]
+    lib.grouped_skinny_gemm_fp8.argtypes = [i32, i32, i32, i32, i32, p, p, p, p, p, p, i32, p, p, p]
+    lib.skinny_moe_fp8_step.argtypes = [ctypes.POINTER(SgMoeFp8Step), p, sz, p]
+    lib.skinny_moe_fp8_step_workspace.argtypes = [i32, i32, i32, i32, i32]
+    for name in ("skinny_gemm_fp8_block_workspace", "skinny_moe_sort_workspace",
+                 "skinny_moe_fp8_step_workspace"):
+        getattr(lib, name).restype = sz
     lib.skinny_moe_step_workspace.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.skinny_moe_step_workspace.restype = sz
     lib.skinny_moe_step.argtypes = [ctypes.POINTER(SgMoeStep), p, sz, p, p, p, p]
@@ -138,7 +167,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "skinny_gemm_residual", "skinny_gemm_noalloc", "grouped_skinny_gemm", "skinny_gemm_prefetch",
                  "skinny_gemm_router_topk", "skinny_moe_step", "skinny_gemm_mxfp4",
                  "skinny_gemm_fp8", "skinny_rmsnorm", "skinny_quant_int8", "skinny_gemm_int8",
-                 "skinny_mlp_int8_step"):
+                 "skinny_mlp_int8_step", "skinny_quant_fp8", "skinny_gemm_fp8_block",
+                 "skinny_moe_sort", "skinny_moe_gather", "skinny_moe_combine",
+                 "skinny_moe_combine_grad", "grouped_skinny_gemm_fp8", "skinny_moe_fp8_step"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

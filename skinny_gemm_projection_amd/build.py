@@ -24,7 +24,8 @@ ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "plan.cpp", "moe_step.cpp", "rowdot.hip", "splitk_mfma.hip", "reduce.hip", "moe.hip", "router.hip", "mxfp4.hip",
            "prefetch.hip", "fp8.hip", "noalloc.hip", "lowp_chunk.hip",
-           "probe.hip", "int8_api.cpp", "int8.hip", "norm_quant.hip"]
+           "probe.hip", "int8_api.cpp", "int8.hip", "norm_quant.hip",
+           "fp8_block_api.cpp", "fp8_block.hip", "quant_fp8.hip", "moe_rows.hip"]
 
 
 def hipcc() -> str:

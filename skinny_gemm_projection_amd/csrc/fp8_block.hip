@@ -1,0 +1,727 @@
+// fp8_block.hip -- product of e4m3 codes with a scale for each block of 128 codes of
+// a row of x and for each 128 x 128 block of W, on gfx950 matrix cores; plain, or
+// over the row segments of routed experts.
+//
+//   y[m,n] = sum_b (sum_{k in block b} xq[m,k] * wq[n,k]) * (xs[b,m] * ws[n/128,b])
+//
+// in fp32 (+ r).  A block's sum is one matrix instruction (or four) with a zero
+// addend; its scale is one fused multiply-add a lane and output.  W is the
+// instruction's first operand and x its second, so a lane holds four neighbours of
+// one row of y and needs one scale a block for all of its channels.
+//
+// Two instructions do the multiplication:
+//  * v_mfma_f32_16x16x128_f8f6f4 takes the codes as they are.  It aligns products of
+//    neighbouring codes to the largest of them and keeps about 14 bits below it, so a
+//    block's sum is off by up to 2^-11 of the sum of its products' magnitudes (2^-16 of
+//    its value on normal data).  It serves bf16 outputs of many rows, which round to
+//    2^-9 themselves, at twice the rate.
+//  * v_mfma_f32_16x16x32_bf16 takes them converted to bf16, exactly, and sums in fp32
+//    (off by 2^-23).  It serves fp32 outputs, and small batches, whose time is the
+//    weight stream's.
+#include "launch.h"
+#include "tile_device.h"
+
+namespace sg {
+
+namespace {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+constexpr int kBlockK = 128;     // codes of a scale
+constexpr int kMaxBlocks = 512;  // K <= 65536
+
+struct Codes32 {  // a lane's 32 codes of a block: two 16-byte pieces
+    uint4 p[2];
+};
+
+// 16 codes as bf16 (exact)
+__device__ __forceinline__ void widen(const uint4 c, uint4 (&v)[2]) {
+    const uint32_t d[4] = {c.x, c.y, c.z, c.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[2 * i] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d[i], 1.0f, false));
+        o[2 * i + 1] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d[i], 1.0f, true));
+    }
+    v[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    v[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Operand registers of a block of 16 rows x 128 codes: as read, or widened.
+template <bool WIDE>
+struct Frag {
+    uint4 v[WIDE ? 4 : 2];
+    __device__ __forceinline__ void set(int piece, const uint4 c) {
+        if constexpr (WIDE) {
+            uint4 w[2];
+            widen(c, w);
+            v[2 * piece] = w[0];
+            v[2 * piece + 1] = w[1];
+        } else {
+            v[piece] = c;
+        }
+    }
+};
+
+// The block's sum of products.
+template <bool WIDE>
+__device__ __forceinline__ f32x4_t block_sum(const Frag<WIDE>& w, const Frag<WIDE>& x) {
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w.v[i]),
+                                                        __builtin_bit_cast(bf16x8_t, x.v[i]), s, 0, 0, 0);
+    } else {
+        struct Two {
+            uint4 a, b;
+        };
+        const i32x8_t a = __builtin_bit_cast(i32x8_t, Two{w.v[0], w.v[1]});
+        const i32x8_t b = __builtin_bit_cast(i32x8_t, Two{x.v[0], x.v[1]});
+        // zero scale operands: the form without scales
+        s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, s, 0, 0, 0, 0, 0, 0);
+    }
+    return s;
+}
+
+__device__ __forceinline__ void add_scaled(f32x4_t& acc, const f32x4_t s, float f) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] = fmaf(s[v], f, acc[v]);
+}
+
+// ------------------------------------------------------------- experts' segments
+
+struct Segment {
+    int e, begin, count;
+};
+
+// Rows [begin, begin + count) of expert e, kept inside [0, rows) whatever the table says.
+__device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ offsets, int e, int rows) {
+    const int lo = min(max(offsets[e], 0), rows), hi = min(max(offsets[e + 1], lo), rows);
+    return Segment{e, lo, hi - lo};
+}
+
+// Exclusive sum of v over the workgroup's threads, and the sum of all.
+template <int THREADS>
+__device__ __forceinline__ int block_sums(int v, int* total) {
+    __shared__ int32_t part[THREADS / kWave];
+    const int lane = threadIdx.x & (kWave - 1);
+    int inc = v;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int u = __shfl_up(inc, d, kWave);
+        if (lane >= d) inc += u;
+    }
+    if (lane == kWave - 1) part[threadIdx.x >> 6] = inc;
+    __syncthreads();
+    int base = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / kWave; ++w) {
+        base += w < (int)(threadIdx.x >> 6) ? part[w] : 0;
+        all += part[w];
+    }
+    *total = all;
+    return base + inc - v;
+}
+
+// The unit that a workgroup takes: segments are cut into units (a unit of BM rows, or
+// one unit a segment), numbered expert by expert.  choose(total units) gives the
+// workgroup's unit, or -1.  All threads return the same (count 0: nothing to do);
+// *first: the segment's first unit's number.
+template <int THREADS, class Units, class Choose>
+__device__ __forceinline__ Segment find_unit(const int32_t* __restrict__ offsets, int E, int rows,
+                                             Units units, Choose choose, int* unit, int* first) {
+    __shared__ int32_t found[4];
+    const int per = (E + THREADS - 1) / THREADS;
+    const int e0 = min(E, (int)threadIdx.x * per), e1 = min(E, e0 + per);
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) mine += units(segment_of(offsets, e, rows).count);
+    if (threadIdx.x == 0) found[2] = 0;
+    int total;
+    int at = block_sums<THREADS>(mine, &total);
+    const int u = choose(total);
+    *unit = u;
+    if (u >= at && u < at + mine) {
+        for (int e = e0; e < e1; ++e) {
+            const Segment s = segment_of(offsets, e, rows);
+            const int n = units(s.count);
+            if (u < at + n) {
+                found[0] = e, found[1] = s.begin, found[2] = s.count, found[3] = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    *first = __builtin_amdgcn_readfirstlane(found[3]);
+    return Segment{__builtin_amdgcn_readfirstlane(found[0]),
+                   __builtin_amdgcn_readfirstlane(found[1]),
+                   u < 0 ? 0 : __builtin_amdgcn_readfirstlane(found[2])};
+}
+
+// Row of x (times its pitch) that row i of an expert's segment reads: kPastEnd if there is none.
+__device__ __forceinline__ uint32_t gathered(const Fp8Product& a, const Segment& s, int i,
+                                             uint32_t pitch) {
+    if (i >= s.count) return kPastEnd;
+    const int t = a.pairs[s.begin + i] / a.topk;
+    return a.pairs[s.begin + i] >= 0 && t < a.x_rows ? (uint32_t)t * pitch : kPastEnd;
+}
+
+// ---------------------------------------------------------------- team kernel
+
+// S waves share 16 rows of W and up to 16 * MT rows of x; wave s takes the blocks
+// s, s + S, ... of K through two LDS slots of its own, W and x both, without a barrier
+// until the sums meet.  Slots are refilled without a condition (past the end a load
+// reads zeros and no memory), so each wait covers the older slot alone.  A load
+// instruction covers 8 rows x 128 bytes, whole lines; piece p of row r sits at place
+// p ^ (r % 8).  An expert's segment is walked 16 * MT rows at a time.
+template <int S, int MT, bool GROUPED>
+__global__ __launch_bounds__(S* kWave) void fp8_team_kernel(Fp8Product a) {
+    constexpr int P = kBlockK / 16, kRows = 8;
+    constexpr int kSlot = 16 * (1 + MT) * P;
+    static_assert(kSlot >= MT * kWave, "a wave's sums reuse its first slot");
+    __shared__ uint4 slot0[S][kSlot], slot1[S][kSlot];
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id_in_block();
+    const int row = lane & 15, grp = lane >> 4;
+    const int K = a.K, N = a.N, Kb = (K + kBlockK - 1) / kBlockK;
+    const int n0 = blockIdx.x * 16;
+    Segment seg{0, 0, a.M};
+    const uint8_t* wq = a.wq;
+    const float* ws = a.ws + (int64_t)(n0 / kBlockK) * Kb;
+    if constexpr (GROUPED) {
+        int unit, first;
+        seg = find_unit<S * kWave>(
+            a.offsets, a.E, a.M, [](int n) { return n > 0 ? 1 : 0; },
+            [](int total) { return (int)blockIdx.y < total ? (int)blockIdx.y : -1; }, &unit, &first);
+        if (seg.count == 0) return;
+        wq += (int64_t)seg.e * N * K;
+        ws += (int64_t)seg.e * ((N + kBlockK - 1) / kBlockK) * Kb;
+    }
+    const rsrc_t rw = make_rsrc(wq + (int64_t)n0 * K, (uint32_t)min(16, N - n0) * (uint32_t)K);
+    const int lrow = lane / P, kpos = ((lane % P) ^ lrow) * 16;
+    const int rounds = max(2, (Kb + S - 1) / S + ((Kb + S - 1) / S & 1));  // an even number
+
+    for (int m0 = 0; m0 < seg.count; m0 += 16 * MT) {
+        const int here = min(16 * MT, seg.count - m0);
+        const bool gather = GROUPED && a.pairs;
+        const int64_t base = gather ? 0 : seg.begin + m0;
+        const rsrc_t rx = make_rsrc(a.xq + base * K, (uint32_t)(gather ? a.x_rows : here) * (uint32_t)K);
+        uint32_t xrow[2 * MT], srow[MT];  // this lane's rows: of the loads, of the scales
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            const int r = i * kRows + lrow;
+            xrow[i] = gather ? gathered(a, seg, m0 + r, K) : r < here ? (uint32_t)(r * K) : kPastEnd;
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int r = j * 16 + row;
+            srow[j] = gather ? gathered(a, seg, m0 + r, 4) : r < here ? (uint32_t)r * 4u : kPastEnd;
+        }
+        f32x4_t acc[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        float f0[MT], f1[MT], w0, w1;
+        auto load = [&](int round, uint4* slot, float (&f)[MT], float& wf) {
+            const int b = round * S + wave, k = b * kBlockK + kpos;
+            const uint32_t at = k < K ? (uint32_t)lrow * K + k : kPastEnd;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                load_to_lds<kStream>(rw, slot + i * kWave, at + (uint32_t)(i * kRows * K));
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i)
+                load_to_lds<kCached>(rx, slot + 16 * P + i * kWave,
+                                     k < K && xrow[i] != kPastEnd ? xrow[i] + k : kPastEnd);
+            const bool in = b < Kb;
+            const rsrc_t rs = make_rsrc(a.xs + (in ? (int64_t)b * a.x_rows + base : 0),
+                                        in ? (uint32_t)(gather ? a.x_rows : here) * 4u : 0u);
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+                f[j] = as_f(__builtin_amdgcn_raw_buffer_load_b32(rs, srow[j], 0, 0));
+            wf = in ? ws[b] : 0.0f;
+        };
+        auto multiply = [&](const uint4* slot, const float (&f)[MT], float wf) {
+            Frag<true> w;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) w.set(t, slot[row * P + ((t * 4 + grp) ^ (row & 7))]);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                Frag<true> x;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    x.set(t, slot[((1 + j) * 16 + row) * P + ((t * 4 + grp) ^ (row & 7))]);
+                add_scaled(acc[j], block_sum(w, x), f[j] * wf);
+                asm volatile("" : "+v"(acc[j]));  // before the refill, whose loads the factors await
+            }
+        };
+        load(0, slot0[wave], f0, w0);
+        load(1, slot1[wave], f1, w1);
+        for (int r = 0; r < rounds; r += 2) {
+            multiply(slot0[wave], f0, w0);
+            reads_done();
+            load(r + 2, slot0[wave], f0, w0);
+            multiply(slot1[wave], f1, w1);
+            reads_done();
+            load(r + 3, slot1[wave], f1, w1);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the end
+#pragma unroll
+        for (int j = 0; j < MT; ++j) slot0[wave][j * kWave + lane] = __builtin_bit_cast(uint4, acc[j]);
+        __syncthreads();
+        for (int e = threadIdx.x; e < MT * kWave; e += S * kWave) {
+            const int l = e & 63, m = (e >> 6) * 16 + (l & 15), n = n0 + 4 * (l >> 4);
+            if (m >= here || n >= N) continue;
+            float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const f32x4_t p = __builtin_bit_cast(f32x4_t, slot0[s][e]);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) y[v] += p[v];
+            }
+            finish4(a, N, seg.begin + m0 + m, n, y);
+        }
+        __syncthreads();  // the sums are read before the slots are filled again
+    }
+}
+
+// ---------------------------------------------------------------- tile kernel
+
+enum TileOut { kTileFinal, kTilePartial, kTileGated };
+
+// Geometry of a tile variant: WM x WN waves, each FM 16-row tiles of x times FN of W;
+// NB stage buffers of one block of K.
+template <int WM_, int WN_, int FM_, int FN_, int NB_>
+struct Fp8Tile {
+    static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, NB = NB_;
+    static constexpr int W = WM * WN, BM = WM * FM * 16, BN = WN * FN * 16;
+    static constexpr int kPieces = kBlockK / 16, kRowsPerLoad = 8;
+    static constexpr int LX = BM / kRowsPerLoad / W, LW = BN / kRowsPerLoad / W;
+    static_assert(LX * kRowsPerLoad * W == BM && LW * kRowsPerLoad * W == BN, "whole loads a wave");
+    static_assert(NB >= 2 && NB <= 4 && W * kWave >= BM, "stage buffers; a scale a thread");
+    static_assert(FN * 16 <= kBlockK && kBlockK % (FN * 16) == 0, "a wave's channels in one block");
+    static constexpr int kStage = (BM + BN) * kPieces;  // 16-byte pieces
+    static constexpr int kWScales = BN > kBlockK ? BN / kBlockK : 1;
+};
+
+template <class T, int OUT, bool GROUPED, bool WIDE>
+__global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kernel(
+    Fp8Product a, int tiles, int per_xcd, int group, int kc, float* partial) {
+    constexpr int BM = T::BM, BN = T::BN, NB = T::NB, FM = T::FM, FN = T::FN, P = T::kPieces;
+    constexpr int kRows = T::kRowsPerLoad, kThreads = T::W * kWave;
+    constexpr bool kGated = OUT == kTileGated;
+    // An array for each stage buffer: the compiler then knows that a load into one of
+    // them does not delay reads of another.
+    __shared__ uint4 b0[T::kStage], b1[T::kStage], b2[NB > 2 ? T::kStage : 1],
+        b3[NB > 3 ? T::kStage : 1];
+    auto buffer = [&](auto i) -> uint4* {
+        constexpr int I = decltype(i)::value % NB;
+        if constexpr (I == 0) return b0;
+        if constexpr (I == 1) return b1;
+        if constexpr (I == 2) return b2;
+        if constexpr (I == 3) return b3;
+    };
+    // scales of x, a stage each
+    __shared__ float x0[kThreads], x1[kThreads], x2[NB > 2 ? kThreads : 1], x3[NB > 3 ? kThreads : 1];
+    auto scales = [&](auto i) -> float* {
+        constexpr int I = decltype(i)::value % NB;
+        if constexpr (I == 0) return x0;
+        if constexpr (I == 1) return x1;
+        if constexpr (I == 2) return x2;
+        if constexpr (I == 3) return x3;
+    };
+    __shared__ float sw[T::kWScales][kMaxBlocks];  // scales of W
+
+    const int N = a.N, K = a.K, Kb = (K + kBlockK - 1) / kBlockK;
+    // a gated tile is BN / 2 outputs wide: 16 gate rows, then their 16 up rows
+    constexpr int BC = kGated ? BN / 2 : BN;
+    const int nn = (N + BC - 1) / BC;
+    Segment seg{0, 0, a.M};
+    int t, m0, n0;
+    if constexpr (GROUPED) {
+        int v, first;
+        seg = find_unit<kThreads>(
+            a.offsets, a.E, a.M, [](int n) { return (n + BM - 1) / BM; },
+            [&](int units) {
+                const int total = units * nn, per = (total + kXcds - 1) / kXcds;
+                const int slot = blockIdx.x / kXcds;
+                t = (int)(blockIdx.x % kXcds) * per + slot;
+                return slot < per && t < total ? t / nn : -1;
+            },
+            &v, &first);
+        if (seg.count == 0) return;
+        // tiles of an expert: down its rows before the next tile of its W
+        const int in = t - first * nn, mt = (seg.count + BM - 1) / BM;
+        m0 = in % mt * BM, n0 = in / mt * BC;
+    } else {
+        // Workgroups reach the 8 XCDs in turn: each XCD takes a run of consecutive
+        // tiles, and a run goes down `group` tiles of x before the next tile of W, so
+        // the tiles in flight on an XCD share rows of both through its L2.
+        t = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
+        if (t >= tiles) return;
+        const int nm = (a.M + BM - 1) / BM;
+        const int first = t / (group * nn) * group, in = t - first * nn;
+        const int rows = min(group, nm - first);
+        m0 = (first + in % rows) * BM, n0 = in / rows * BC;
+    }
+    const int kbeg = blockIdx.y * kc, kend = min(K, kbeg + kc);
+    const int here = min(BM, seg.count - m0);
+    const bool gather = GROUPED && a.pairs;
+    const int64_t base = gather ? 0 : seg.begin + m0;  // row of x of the tile's first
+    const int64_t wbase = (int64_t)seg.e * (kGated ? 2 : 1) * N;  // row of W
+
+    const int lane = threadIdx.x & (kWave - 1), w = wave_id_in_block();
+    const rsrc_t rx = make_rsrc(a.xq + base * K, (uint32_t)(gather ? a.x_rows : here) * (uint32_t)K);
+    const uint32_t wbytes = (uint32_t)min(BC, N - n0) * (uint32_t)K;
+    const rsrc_t rw = make_rsrc(a.wq + (wbase + n0) * K, wbytes);
+    const rsrc_t ru = make_rsrc(a.wq + (wbase + n0 + (kGated ? N : 0)) * K, wbytes);
+    {
+        const int nb = (N + kBlockK - 1) / kBlockK;  // gated: N is a multiple of 128
+        const float* ws = a.ws + (int64_t)seg.e * (kGated ? 2 : 1) * nb * Kb;
+        const int b_beg = kbeg / kBlockK, b_end = (kend + kBlockK - 1) / kBlockK;
+#pragma unroll
+        for (int i = 0; i < T::kWScales; ++i) {
+            const int at = kGated ? n0 / kBlockK + i * nb : n0 / kBlockK + i;
+            const bool in = kGated || at < nb;
+            for (int b = b_beg + threadIdx.x; b < b_end; b += kThreads)
+                sw[i][b - b_beg] = in ? ws[(int64_t)at * Kb + b] : 0.0f;
+            if (b_beg >= b_end && threadIdx.x == 0) sw[i][0] = 0.0f;  // K = 0
+        }
+    }
+    // Piece p of row r sits at place p ^ (r % 8) of the row: 8 neighbouring rows of one
+    // piece meet every bank once.
+    const int lrow = lane / P, kpos = ((lane % P) ^ lrow) * 16;
+    const uint32_t lbase = (uint32_t)lrow * K + kpos + kbeg;
+    const int klen = kend - kbeg - kpos;
+    uint32_t xrow[T::LX], srow;
+    if constexpr (GROUPED) {
+#pragma unroll
+        for (int i = 0; i < T::LX; ++i) {
+            const int r = (w * T::LX + i) * kRows + lrow;
+            xrow[i] = gather ? gathered(a, seg, m0 + r, K) : r < here ? (uint32_t)(r * K) : kPastEnd;
+            if (xrow[i] != kPastEnd) xrow[i] += kpos;
+        }
+    }
+    {
+        const int r = threadIdx.x;
+        srow = r >= BM ? kPastEnd
+                       : gather ? gathered(a, seg, m0 + r, 4) : r < here ? (uint32_t)r * 4u : kPastEnd;
+    }
+    auto issue = [&](uint4* b, float* s, int k0) {
+        const uint32_t at = k0 < klen ? lbase : kPastEnd;
+#pragma unroll
+        for (int i = 0; i < T::LX; ++i) {
+            const int r = (w * T::LX + i) * kRows;
+            uint32_t off = at + (uint32_t)(r * K + k0);
+            if constexpr (GROUPED)
+                off = k0 < klen && xrow[i] != kPastEnd ? xrow[i] + (uint32_t)k0 : kPastEnd;
+            load_to_lds<kCached>(rx, b + r * P, off);
+        }
+#pragma unroll
+        for (int i = 0; i < T::LW; ++i) {
+            const int r = (w * T::LW + i) * kRows;
+            const bool up = kGated && r % 32 >= 16;
+            const int src = kGated ? r / 32 * 16 + r % 16 : r;
+            load_to_lds<kCached>(up ? ru : rw, b + (BM + r) * P, at + (uint32_t)(src * K + k0));
+        }
+        const int kb = min((kbeg + k0) / kBlockK, max(Kb - 1, 0));
+        const rsrc_t rs = make_rsrc(a.xs + (int64_t)kb * a.x_rows + base,
+                                    kbeg + k0 < kend ? (uint32_t)(gather ? a.x_rows : here) * 4u : 0u);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(s + w * kWave), 4, (int)srow, 0, 0,
+                                                 kCached);
+    };
+
+    f32x4_t acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int row = lane & 15, grp = lane >> 4, wm = w / T::WN, wn = w % T::WN;
+    const int xat = (wm * FM * 16 + row) * P, wat = (BM + wn * FN * 16 + row) * P;
+    const int p0 = grp ^ (row & 7), p1 = (4 + grp) ^ (row & 7);
+    constexpr int kLoads = T::LX + T::LW + 1, kOut = (NB - 2) * kLoads;
+    const int n = max(1, (kend - kbeg + kBlockK - 1) / kBlockK);
+    // Stage s: wait until it has landed for every wave, refill the buffer of stage s - 1
+    // (all its reads are done) with stage s + NB - 1, multiply.
+    // The products of one 16-row tile of x run while the sums of the tile before (of the
+    // stage before, for the first) are scaled and added.
+    constexpr int kScales = kGated ? 2 : 1;
+    static_assert(FM % 2 == 0, "the tiles of x alternate between two sets of sums");
+    f32x4_t part[2][FN];
+    float f[2][kScales] = {};
+#pragma unroll
+    for (int c = 0; c < FN; ++c) part[1][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    auto stage = [&](auto i, int s) {  // s % NB == i
+        constexpr int J = (decltype(i)::value + NB - 1) % NB;
+        const uint4* b = buffer(i);
+        const float* sx = scales(i);
+        wait_and_barrier<kOut>();
+        issue(buffer(std::integral_constant<int, J>{}), scales(std::integral_constant<int, J>{}),
+              (s + NB - 1) * kBlockK);
+        float ws[kScales];
+#pragma unroll
+        for (int c = 0; c < kScales; ++c)
+            ws[c] = sw[kGated ? c : wn * FN * 16 / kBlockK][s];
+        Frag<WIDE> fw[FN], fx[2];
+        auto read_x = [&](auto j) {
+            constexpr int J = decltype(j)::value;
+            fx[J % 2].set(0, b[xat + J * 16 * P + p0]);
+            fx[J % 2].set(1, b[xat + J * 16 * P + p1]);
+        };
+#pragma unroll
+        for (int c = 0; c < FN; ++c) {
+            fw[c].set(0, b[wat + c * 16 * P + p0]);
+            fw[c].set(1, b[wat + c * 16 * P + p1]);
+        }
+        read_x(std::integral_constant<int, 0>{});
+        __builtin_amdgcn_sched_barrier(0);
+        unrolled<0, FM>([&](auto jc) {
+            constexpr int j = decltype(jc)::value, prev = (j + FM - 1) % FM;
+            if constexpr (j + 1 < FM) read_x(std::integral_constant<int, j + 1>{});
+            const float xs = sx[(wm * FM + j) * 16 + row];
+#pragma unroll
+            for (int c = 0; c < FN; ++c) {
+                part[j % 2][c] = block_sum(fw[c], fx[j % 2]);
+                add_scaled(acc[c][prev], part[(j + 1) % 2][c], f[(j + 1) % 2][c % kScales]);
+                asm volatile("" : "+v"(acc[c][prev]));  // added here, not behind the stage
+            }
+#pragma unroll
+            for (int c = 0; c < kScales; ++c) f[j % 2][c] = xs * ws[c];
+            if constexpr (j + 1 < FM) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);  // LDS reads
+#pragma unroll
+            for (int c = 0; c < FN; ++c) {
+                __builtin_amdgcn_sched_group_barrier(0x8, WIDE ? 4 : 1, 0);  // matrix instructions
+                __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);             // vector arithmetic
+            }
+            __builtin_amdgcn_sched_barrier(0);  // reads stay one tile ahead: more would not fit
+        });
+    };
+    unrolled<0, NB - 1>([&](auto i) {
+        issue(buffer(i), scales(i), decltype(i)::value * kBlockK);
+    });
+    int s = 0;
+    for (; s + NB <= n; s += NB)
+        unrolled<0, NB>([&](auto i) { stage(i, s + decltype(i)::value); });
+    unrolled<0, NB - 1>([&](auto i) {
+        if (s + decltype(i)::value < n) stage(i, s + decltype(i)::value);
+    });
+#pragma unroll
+    for (int c = 0; c < FN; ++c) add_scaled(acc[c][FM - 1], part[1][c], f[1][c % kScales]);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may outlive the workgroup's LDS
+
+    if constexpr (OUT == kTilePartial) {
+        float* out = partial + ((int64_t)blockIdx.y * tiles + t) * (BM * BN);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+                if ((wm * FM + j) * 16 < here)
+                    reinterpret_cast<f32x4_t*>(out)[((w * FN + i) * FM + j) * kWave + lane] = acc[i][j];
+    } else if constexpr (OUT == kTileFinal) {
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int ml = (wm * FM + j) * 16 + row;
+            if (ml >= here) continue;
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                const int c = n0 + (wn * FN + i) * 16 + grp * 4;
+                if (c >= N) continue;
+                float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                finish4(a, N, seg.begin + m0 + ml, c, y);
+            }
+        }
+    }
+}
+
+// Sums the S partial tiles of fp8_tile_kernel<T, kTilePartial> in order and finishes the
+// outputs; a thread owns the four neighbours a lane of the tile kernel held.
+template <class T>
+__global__ __launch_bounds__(kBlock) void fp8_reduce_kernel(const float* __restrict__ partial,
+                                                            Fp8Product a, int tiles, int group,
+                                                            int S) {
+    constexpr int BM = T::BM, BN = T::BN, FM = T::FM, FN = T::FN;
+    constexpr int kFrags = T::W * FM * FN;  // 16 x 16 blocks of a tile
+    const int64_t e = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    const int t = (int)(e / (kFrags * kWave)), f = (int)(e / kWave) % kFrags, lane = (int)e & 63;
+    if (t >= tiles) return;
+    const int nn = (a.N + BN - 1) / BN, nm = (a.M + BM - 1) / BM;
+    const int first = t / (group * nn) * group, in = t - first * nn;
+    const int rows = min(group, nm - first);
+    const int m0 = (first + in % rows) * BM, n0 = in / rows * BN;
+    const int w = f / (FM * FN), i = f / FM % FN, j = f % FM;
+    const int m = m0 + ((w / T::WN) * FM + j) * 16 + (lane & 15);
+    const int n = n0 + ((w % T::WN) * FN + i) * 16 + (lane >> 4) * 4;
+    if (m >= a.M || n >= a.N) return;
+    const f32x4_t* p =
+        reinterpret_cast<const f32x4_t*>(partial) + ((int64_t)t * kFrags + f) * kWave + lane;
+    const int64_t step = (int64_t)tiles * (BM * BN / 4);
+    f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    int s = 0;
+    for (; s + 4 <= S; s += 4) {
+        const f32x4_t q0 = p[s * step], q1 = p[(s + 1) * step], q2 = p[(s + 2) * step],
+                      q3 = p[(s + 3) * step];
+        sum = (((sum + q0) + q1) + q2) + q3;
+    }
+    for (; s < S; ++s) sum += p[s * step];
+    float y[4] = {sum[0], sum[1], sum[2], sum[3]};
+    finish4(a, a.N, m, n, y);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tile variants, BM x BN: 256 x 256, 128 x 256, 128 x 128, 64 x 128.
+typedef Fp8Tile<2, 4, 8, 4, 2> Tile256;
+typedef Fp8Tile<2, 4, 4, 4, 3> Tile128w;
+typedef Fp8Tile<2, 4, 4, 2, 4> Tile128;
+typedef Fp8Tile<2, 2, 2, 4, 3> Tile64;
+
+template <class F>
+void with_tile(int v, F f) {
+    switch (v) {
+        case 0: f(Tile256{}); break;
+        case 1: f(Tile128w{}); break;
+        case 2: f(Tile128{}); break;
+        default: f(Tile64{}); break;
+    }
+}
+
+struct TileCost {
+    int bm, bn;
+    int per_cu;      // workgroups a compute unit holds
+    int group;       // tiles of x an XCD's run goes down before the next tile of W
+    double full;     // ns per code of K of a round that fills every compute unit
+    double single;   // of a round with at most one workgroup a compute unit
+};
+constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.0, 9.9},
+                               {128, 256, 1, 8, 7.2, 6.2},
+                               {128, 128, 1, 8, 4.1, 3.9},
+                               {64, 128, 2, 8, 6.4, 3.6}};
+constexpr int kTileVariants = 4;
+constexpr int kCus = 256;
+constexpr int kTeamMaxM = 64;
+
+template <class T, int OUT, bool WIDE>
+void launch_tiles(const Fp8Product& a, int S, int kc, int group, float* partial, hipStream_t stream) {
+    const int tiles = (int)(ceil_div(a.M, T::BM) * ceil_div(a.N, T::BN));
+    const int per = (int)ceil_div(tiles, kXcds);
+    hipLaunchKernelGGL((fp8_tile_kernel<T, OUT, false, WIDE>), dim3(per * kXcds, S),
+                       dim3(T::W * kWave), 0, stream, a, tiles, per, group, kc, partial);
+}
+
+template <class T, bool WIDE>
+void launch_plain(const Fp8Product& a, int S, int kc, int group, void* ws, hipStream_t stream) {
+    float* partial = static_cast<float*>(ws);
+    if (S <= 1) {
+        launch_tiles<T, kTileFinal, WIDE>(a, 1, a.K, group, nullptr, stream);
+        return;
+    }
+    launch_tiles<T, kTilePartial, WIDE>(a, S, kc, group, partial, stream);
+    const int tiles = (int)(ceil_div(a.M, T::BM) * ceil_div(a.N, T::BN));
+    const int64_t threads = (int64_t)tiles * (T::BM * T::BN / 4);
+    hipLaunchKernelGGL((fp8_reduce_kernel<T>), dim3((uint32_t)ceil_div(threads, kBlock)), dim3(kBlock), 0,
+                       stream, partial, a, tiles, group, S);
+}
+
+// Tiles of a grouped product, whatever its segments: at most this many.
+template <class T>
+int64_t most_tiles(int M, int E, int N) {
+    return ((int64_t)M / T::BM + (E < M ? E : M)) * ceil_div(N, T::BN);
+}
+
+template <class T, bool WIDE>
+void launch_grouped_tiles(const Fp8Product& a, hipStream_t stream) {
+    const int64_t tiles = most_tiles<T>(a.M, a.E, a.N);
+    hipLaunchKernelGGL((fp8_tile_kernel<T, kTileFinal, true, WIDE>),
+                       dim3((uint32_t)(ceil_div(tiles, kXcds) * kXcds)), dim3(T::W * kWave), 0, stream, a,
+                       0, 0, 0, a.K, nullptr);
+}
+
+template <bool GROUPED>
+void launch_team(int mt, const Fp8Product& a, hipStream_t stream) {
+    constexpr int S = 8;
+    const dim3 grid((uint32_t)ceil_div(a.N, 16), GROUPED ? (a.E < a.M ? a.E : a.M) : 1), block(S * kWave);
+    if (mt == 1) {
+        hipLaunchKernelGGL((fp8_team_kernel<S, 1, GROUPED>), grid, block, 0, stream, a);
+    } else if (mt == 2 || GROUPED) {
+        hipLaunchKernelGGL((fp8_team_kernel<S, 2, GROUPED>), grid, block, 0, stream, a);
+    } else if constexpr (!GROUPED) {
+        if (mt == 3)
+            hipLaunchKernelGGL((fp8_team_kernel<S, 3, GROUPED>), grid, block, 0, stream, a);
+        else
+            hipLaunchKernelGGL((fp8_team_kernel<S, 4, GROUPED>), grid, block, 0, stream, a);
+    }
+}
+
+}  // namespace
+
+Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide) {
+    if (M <= kTeamMaxM) return Fp8BlockPlan{Fp8BlockPlan::kTeam, (M + 15) / 16, 0, 1, K, 0};
+    Fp8BlockPlan best{};
+    double least = 1e30;
+    for (int v = wide ? 1 : 0; v < kTileVariants; ++v) {
+        const TileCost& c = kTiles[v];
+        const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn);
+        for (int S = 1; S <= 16; ++S) {
+            const int kc = S == 1 ? K : (int)ceil_div(ceil_div(K, S), kBlockK) * kBlockK;
+            if (S > 1 && (kc < 4 * kBlockK || (int64_t)(S - 1) * kc >= K)) break;
+            const int64_t wgs = tiles * S, slots = (int64_t)kCus * c.per_cu, rem = wgs % slots;
+            double est = 3.0 + kc * (wgs / slots * c.full + (rem == 0 ? 0.0 : rem <= kCus ? c.single : c.full)) / 1000.0;
+            const size_t ws = S > 1 ? (size_t)S * tiles * c.bm * c.bn * 4 : 0;
+            if (S > 1) est += 3.0 + 8.0 * S * M * N / 4.0e6;
+            if (est < least && ws <= ((size_t)1 << 30)) {
+                least = est;
+                best = Fp8BlockPlan{Fp8BlockPlan::kTile, 0, v, S, kc, ws};
+            }
+        }
+    }
+    return best;
+}
+
+Fp8BlockPlan fp8_grouped_plan(int M, int E, int N, int K, bool wide) {
+    const int64_t rows = M / (E < M ? E : M);  // an expert's, on average
+    if (rows <= 24)
+        return Fp8BlockPlan{Fp8BlockPlan::kTeam, rows <= 4 ? 1 : 2, 0, 1, K, 0};
+    return Fp8BlockPlan{Fp8BlockPlan::kTile, 0, rows <= 64 ? 3 : rows <= 160 || wide ? 1 : 0, 1, K, 0};
+}
+
+bool fp8_grouped_fits(const Fp8BlockPlan& p, int M, int E, int N) {
+    if (p.kind == Fp8BlockPlan::kTeam) return true;
+    bool fits = false;
+    with_tile(p.tile, [&](auto shape) {  // threads of a launch are counted in 32 bits
+        typedef decltype(shape) T;
+        fits = (most_tiles<T>(M, E, N) + kXcds) * T::W * kWave < ((int64_t)1 << 32);
+    });
+    return fits;
+}
+
+hipError_t launch_fp8_block(const Fp8BlockPlan& p, const Fp8Product& product, void* ws,
+                            hipStream_t stream) {
+    Fp8Product a = product;
+    a.ld = a.N;
+    const bool wide = a.y_f32 != nullptr;
+    if (p.kind == Fp8BlockPlan::kTeam) {
+        if (a.offsets)
+            launch_team<true>(p.mt, a, stream);
+        else
+            launch_team<false>(p.mt, a, stream);
+        return hipGetLastError();
+    }
+    with_tile(p.tile, [&](auto shape) {
+        typedef decltype(shape) T;
+        if (wide) {
+            if constexpr (T::FM * T::FN <= 16) {
+                if (a.offsets)
+                    launch_grouped_tiles<T, true>(a, stream);
+                else
+                    launch_plain<T, true>(a, p.S, p.kc, kTiles[p.tile].group, ws, stream);
+            }
+        } else if (a.offsets) {
+            launch_grouped_tiles<T, false>(a, stream);
+        } else {
+            launch_plain<T, false>(a, p.S, p.kc, kTiles[p.tile].group, ws, stream);
+        }
+    });
+    return hipGetLastError();
+}
+
+}  // namespace sg

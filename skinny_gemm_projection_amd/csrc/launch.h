@@ -209,6 +209,62 @@ bool int8_gated_ok(const Int8Plan& p);
 hipError_t launch_gated_int8(const Int8Plan& p, int M, int F, int H, const int8_t* xq,
                              const int8_t* wq, const Int8Epilogue& ep, hipStream_t stream);
 
+// e4m3 codes [M, K] of rows and their scales [ceil(K/128), M] (quant_fp8.hip): K a
+// multiple of 8; gated: rows of 2K values.
+hipError_t launch_quant_fp8(int M, int K, const void* x, bool f32, bool gated, uint8_t* codes,
+                            float* scales, hipStream_t stream);
+
+// Pairs sorted by expert and rows brought there and back (moe_rows.hip); pitch: bytes
+// of a row, a multiple of 16 below 2^32.  T * topk <= 2^22, E <= 4096.
+size_t moe_sort_workspace_bytes(int64_t P, int E);
+int moe_sort_launches(int64_t P);
+hipError_t launch_moe_sort(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* sorted,
+                           int32_t* positions, void* ws, hipStream_t stream);
+hipError_t launch_moe_gather(const void* x, int T, int topk, int64_t pitch, const int32_t* positions,
+                             void* rows, hipStream_t stream);
+hipError_t launch_moe_combine(const void* rows, int T, int topk, int64_t pitch, bool f32,
+                              const int32_t* positions, const float* w, const void* r, void* out,
+                              hipStream_t stream);
+hipError_t launch_moe_combine_grad(const void* d_out, const void* rows, int T, int topk,
+                                   int64_t pitch, bool f32, const int32_t* positions, const float* w,
+                                   void* d_rows, float* d_w, hipStream_t stream);
+
+// Product of e4m3 codes with block scales (fp8_block.hip): x [M, K], W [N, K] (or
+// [E, N, K]), K a multiple of 16, M, N >= 1.
+struct Fp8Product {
+    const uint8_t* xq;
+    const float* xs;      // [ceil(K/128), x_rows]
+    const uint8_t* wq;
+    const float* ws;      // [ceil(N/128), ceil(K/128)], for experts [E, ..]
+    int M, N, K;          // M: rows of the outputs
+    int x_rows;           // rows of x (M, unless rows are gathered)
+    float* y_f32;         // nullable
+    uint16_t* y_bf16;     // nullable; may equal r
+    const uint16_t* r;    // residual [M, N] or nullptr
+    // routed experts: expert e has the rows [offsets[e], offsets[e + 1])
+    const int32_t* offsets = nullptr;  // [E + 1] or nullptr
+    int E = 0;
+    const int32_t* pairs = nullptr;    // row i reads row pairs[i] / topk of x; or nullptr
+    int topk = 1;
+    // the gated product's codes in the place of y (wq: N gate rows, then N up rows)
+    uint8_t* codes = nullptr;          // [M, N]
+    float* scales = nullptr;           // [N/128, M]
+    int ld = 0;                        // row stride of outputs and residual (set by the launchers)
+};
+// What runs for a size.
+struct Fp8BlockPlan {
+    enum Kind { kTeam, kTile } kind;
+    int mt;                // team kernel: 16-row tiles of x
+    int tile, S, kc;       // tile kernel: variant, K splits, codes a split
+    size_t workspace;      // bytes of fp32 partial sums (S > 1)
+};
+// wide: fp32 outputs are wanted.
+Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide);
+// experts: M pairs over E experts
+Fp8BlockPlan fp8_grouped_plan(int M, int E, int N, int K, bool wide);
+bool fp8_grouped_fits(const Fp8BlockPlan& p, int M, int E, int N);  // in one launch's limits
+hipError_t launch_fp8_block(const Fp8BlockPlan& p, const Fp8Product& a, void* ws, hipStream_t stream);
+
 // Router top-k: ids [T,k] (and their scores) from fp32 scores, row t at
 // scores + t*ld (ld >= E); E <= 4096, k <= 32 (checked by the caller).
 hipError_t launch_router_topk(const float* scores, int64_t ld, int T, int E, int k,

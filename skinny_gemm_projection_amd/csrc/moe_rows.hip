@@ -1,0 +1,412 @@
+// moe_rows.hip -- (token, slot) pairs sorted by expert, token rows laid out in that
+// order, and expert outputs brought back to their tokens with the routing weights;
+// the gradients of both.
+//
+// Pair p = t * topk + j belongs to expert ids[p].  The sort is a counting sort,
+// stable in p:
+//   offsets[e]   = number of pairs of experts below e,
+//   positions[p] = offsets[ids[p]] + number of pairs q < p with ids[q] == ids[p],
+//   sorted[positions[p]] = p,
+// and pairs whose id is outside [0, E) are left out (position -1).  The place of a
+// pair follows from the ids alone, no atomic decides an order.
+//
+//   gather:   rows[positions[t, j]] = x[t]
+//   combine:  out[t] = (r[t] +) sum_j w[t, j] * rows[positions[t, j]]
+//   combine's gradient: d_rows[positions[t, j]] = w[t, j] * d_out[t],
+//                       d_w[t, j] = <d_out[t], rows[positions[t, j]]>
+//   gather's gradient is combine without weights.
+// A pair has one row and a row one pair, so no two threads write one place.  All
+// row kernels go token by token: the token's own row is read (or written) once, and
+// its topk rows elsewhere once each.
+#include "int8_device.h"
+#include "launch.h"
+
+namespace sg {
+
+namespace {
+
+// ------------------------------------------------------------------ sort
+
+// Inclusive sum over the 64 lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v) {
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int u = __shfl_up(v, d, kWave);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+// s[e] becomes the sum of s[0 .. e), e < n, and the sum of all is returned.
+// Thread t owns the entries [t * per, (t + 1) * per).
+template <int THREADS>
+__device__ __forceinline__ int exclusive_scan(int32_t* s, int n) {
+    __shared__ int32_t part[THREADS / kWave];
+    const int per = (n + THREADS - 1) / THREADS;
+    const int lo = min(n, (int)threadIdx.x * per), hi = min(n, lo + per);
+    int sum = 0;
+    for (int e = lo; e < hi; ++e) sum += s[e];
+    const int inc = wave_scan(sum);
+    if ((threadIdx.x & (kWave - 1)) == kWave - 1) part[threadIdx.x >> 6] = inc;
+    __syncthreads();
+    int base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / kWave; ++w) {
+        const int v = part[w];
+        base += w < (int)(threadIdx.x >> 6) ? v : 0;
+        total += v;
+    }
+    int run = base + inc - sum;
+    for (int e = lo; e < hi; ++e) {
+        const int v = s[e];
+        s[e] = run;
+        run += v;
+    }
+    __syncthreads();
+    return total;
+}
+
+// Places of `count` pairs from pair p0 on: cursor[e] holds the next place of
+// expert e.  Waves take 64 pairs each in turn, one wave at a time; inside a wave
+// the lanes of one expert are found by a ballot for each bit of the id.
+template <int THREADS>
+__device__ __forceinline__ void place_pairs(const int32_t* __restrict__ ids, int64_t p0, int count,
+                                            int E, int bits, int32_t* cursor, int32_t* sorted,
+                                            int32_t* positions) {
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id_in_block();
+    for (int c0 = 0; c0 < count; c0 += THREADS) {
+        const int c = c0 + threadIdx.x;
+        const int e = c < count ? ids[p0 + c] : -1;
+        const bool ok = e >= 0 && e < E;
+        uint64_t same = __ballot(ok);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t set = __ballot((e >> b) & 1);
+            same &= (e >> b) & 1 ? set : ~set;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        int at = 0;
+        const int turns = min(THREADS, count - c0);
+        for (int w = 0; w * kWave < turns; ++w) {  // the same number of turns for every wave
+            if (w == wave && ok) {
+                at = cursor[e];
+                // the reads of all lanes are before this write: one wave, in order
+                if (rank == 0) cursor[e] = at + __popcll(same);
+            }
+            __syncthreads();
+        }
+        if (c < count) {
+            positions[p0 + c] = ok ? at + rank : -1;
+            if (ok && sorted) sorted[at + rank] = (int32_t)(p0 + c);
+        }
+    }
+}
+
+__device__ __forceinline__ void count_pairs(const int32_t* __restrict__ ids, int64_t p0, int count,
+                                            int E, int32_t* counts, int threads) {
+    for (int e = threadIdx.x; e < E; e += threads) counts[e] = 0;
+    __syncthreads();
+    for (int c = threadIdx.x; c < count; c += threads) {
+        const int e = ids[p0 + c];
+        if (e >= 0 && e < E) atomicAdd(&counts[e], 1);  // a count: the order is free
+    }
+    __syncthreads();
+}
+
+constexpr int kSortOneMax = 4096;   // pairs one workgroup sorts alone
+constexpr int kSortChunk = 2048;    // pairs of a workgroup beyond
+constexpr int kSortMaxExperts = 4096;
+
+__global__ __launch_bounds__(1024) void moe_sort_one_kernel(const int32_t* __restrict__ ids, int P,
+                                                            int E, int bits, int32_t* offsets,
+                                                            int32_t* sorted, int32_t* positions) {
+    __shared__ int32_t cursor[kSortMaxExperts];
+    count_pairs(ids, 0, P, E, cursor, 1024);
+    const int total = exclusive_scan<1024>(cursor, E);
+    for (int e = threadIdx.x; e < E; e += 1024) offsets[e] = cursor[e];
+    if (threadIdx.x == 0) offsets[E] = total;
+    __syncthreads();  // the offsets are read before the cursors move
+    place_pairs<1024>(ids, 0, P, E, bits, cursor, sorted, positions);
+    if (sorted)
+        for (int i = total + threadIdx.x; i < P; i += 1024) sorted[i] = -1;
+}
+
+// counts[chunk][e] of the pairs of a chunk
+__global__ __launch_bounds__(kBlock) void moe_count_kernel(const int32_t* __restrict__ ids, int P,
+                                                           int E, int32_t* counts) {
+    __shared__ int32_t s[kSortMaxExperts];
+    const int64_t p0 = (int64_t)blockIdx.x * kSortChunk;
+    count_pairs(ids, p0, (int)min((int64_t)kSortChunk, P - p0), E, s, kBlock);
+    for (int e = threadIdx.x; e < E; e += kBlock) counts[(int64_t)blockIdx.x * E + e] = s[e];
+}
+
+// counts[chunk][e] becomes the sum over the chunks before, totals[e] that over all.
+__global__ __launch_bounds__(kWave) void moe_scan_kernel(int32_t* counts, int chunks, int E,
+                                                         int32_t* totals) {
+    const int e = blockIdx.x * kWave + threadIdx.x;
+    if (e >= E) return;
+    int run = 0;
+    int c = 0;
+    for (; c + 8 <= chunks; c += 8) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = counts[(int64_t)(c + i) * E + e];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            counts[(int64_t)(c + i) * E + e] = run;
+            run += v[i];
+        }
+    }
+    for (; c < chunks; ++c) {
+        const int v = counts[(int64_t)c * E + e];
+        counts[(int64_t)c * E + e] = run;
+        run += v;
+    }
+    totals[e] = run;
+}
+
+__global__ __launch_bounds__(kBlock) void moe_place_kernel(const int32_t* __restrict__ ids, int P,
+                                                           int E, int bits,
+                                                           const int32_t* __restrict__ before,
+                                                           const int32_t* __restrict__ totals,
+                                                           int32_t* offsets, int32_t* sorted,
+                                                           int32_t* positions) {
+    __shared__ int32_t cursor[kSortMaxExperts];
+    for (int e = threadIdx.x; e < E; e += kBlock) cursor[e] = totals[e];
+    __syncthreads();
+    const int total = exclusive_scan<kBlock>(cursor, E);
+    for (int e = threadIdx.x; e < E; e += kBlock) {
+        if (blockIdx.x == 0) offsets[e] = cursor[e];
+        cursor[e] += before[(int64_t)blockIdx.x * E + e];
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = total;
+    __syncthreads();
+    const int64_t p0 = (int64_t)blockIdx.x * kSortChunk;
+    const int count = (int)min((int64_t)kSortChunk, P - p0);
+    place_pairs<kBlock>(ids, p0, count, E, bits, cursor, sorted, positions);
+    if (sorted)  // behind the last valid pair
+        for (int i = threadIdx.x; i < count; i += kBlock)
+            if (p0 + i >= total) sorted[p0 + i] = -1;
+}
+
+// ------------------------------------------------------------------ rows
+
+constexpr int kSpan = kBlock * 16;  // bytes of a row a workgroup takes at once
+
+// Workgroups (span, token): tokens go over y and z, whose sizes a launch limits.
+constexpr int kTokensY = 32768;
+__device__ __forceinline__ int64_t token_of() {
+    return (int64_t)blockIdx.z * kTokensY + blockIdx.y;
+}
+
+// A workgroup brings one span of one token's row to its places.
+__global__ __launch_bounds__(kBlock) void moe_gather_kernel(const char* __restrict__ x, int64_t pitch,
+                                                            int T, int topk,
+                                                            const int32_t* __restrict__ positions,
+                                                            char* __restrict__ rows) {
+    const int64_t t = token_of();
+    const int64_t at = (int64_t)blockIdx.x * kSpan + threadIdx.x * 16;
+    const int limit = T * topk;  // rows there are: a position past them is taken as left out
+    if (t >= T || at >= pitch) return;
+    const uint4 v = *reinterpret_cast<const uint4*>(x + t * pitch + at);
+    for (int j = 0; j < topk; ++j) {
+        const int pos = positions[t * topk + j];
+        if (pos >= 0 && pos < limit) *reinterpret_cast<uint4*>(rows + pos * pitch + at) = v;
+    }
+}
+
+template <bool F32>
+struct Piece {  // 16 bytes of a row
+    static constexpr int N = F32 ? 4 : 8;
+    static __device__ __forceinline__ void unpack(const uint4 u, float (&v)[N]) {
+        const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (F32) {
+                v[i] = as_f(d[i]);
+            } else {
+                v[2 * i] = as_f(d[i] << 16);
+                v[2 * i + 1] = as_f(d[i] & 0xffff0000u);
+            }
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[N]) {
+        if constexpr (F32)
+            return make_uint4(as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3]));
+        else
+            return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                              pack_bf16(v[6], v[7]));
+    }
+};
+
+constexpr int kAtOnce = 8;  // rows of a token requested before the first is added
+
+// Sums in fp32, j ascending, each step one fused multiply-add (without weights an
+// addition); the residual is added last and the result rounded once.
+template <bool F32>
+__global__ __launch_bounds__(kBlock) void moe_combine_kernel(
+    const char* __restrict__ rows, int64_t pitch, int T, int topk,
+    const int32_t* __restrict__ positions, const float* __restrict__ w, const char* r,
+    char* out) {  // out may be r
+    typedef Piece<F32> P;
+    const int64_t t = token_of();
+    const int64_t at = (int64_t)blockIdx.x * kSpan + threadIdx.x * 16;
+    const int limit = T * topk;
+    if (t >= T || at >= pitch) return;
+    float acc[P::N] = {};
+    for (int j0 = 0; j0 < topk; j0 += kAtOnce) {
+        uint4 v[kAtOnce];
+        float f[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int j = j0 + i;
+            const int pos = j < topk ? positions[t * topk + j] : -1;
+            const bool on = pos >= 0 && pos < limit;
+            f[i] = on ? w ? w[t * topk + j] : 1.0f : 0.0f;
+            // a left-out pair reads zeros through an empty buffer: no branch around a load
+            v[i] = load16(make_rsrc(rows + (on ? pos : 0) * pitch, on ? (uint32_t)pitch : 0u),
+                          (uint32_t)at);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            float y[P::N];
+            P::unpack(v[i], y);
+#pragma unroll
+            for (int k = 0; k < P::N; ++k) acc[k] = fmaf(f[i], y[k], acc[k]);
+        }
+    }
+    if (r) {
+        float y[P::N];
+        P::unpack(*reinterpret_cast<const uint4*>(r + t * pitch + at), y);
+#pragma unroll
+        for (int k = 0; k < P::N; ++k) acc[k] = y[k] + acc[k];
+    }
+    *reinterpret_cast<uint4*>(out + t * pitch + at) = P::pack(acc);
+}
+
+// One workgroup a token.  The dot products of up to kAtOnce rows are held while the
+// row is walked; d_rows may be rows (an element is read before it is written, by the
+// same thread).
+template <bool F32>
+__global__ __launch_bounds__(kBlock) void moe_combine_grad_kernel(
+    const char* __restrict__ d_out, const char* rows, int64_t pitch, int T, int topk,
+    const int32_t* __restrict__ positions, const float* __restrict__ w, char* d_rows,
+    float* __restrict__ d_w) {
+    typedef Piece<F32> P;
+    __shared__ float part[kWavesPerBlock][kAtOnce];
+    const int64_t t = blockIdx.x;
+    const int limit = T * topk;
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id_in_block();
+    for (int j0 = 0; j0 < topk; j0 += kAtOnce) {
+        int64_t base[kAtOnce];
+        float f[kAtOnce], dot[kAtOnce];
+        bool on[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int j = j0 + i;
+            const int pos = j < topk ? positions[t * topk + j] : -1;
+            on[i] = pos >= 0 && pos < limit;
+            base[i] = on[i] ? pos * pitch : 0;
+            f[i] = on[i] ? w[t * topk + j] : 0.0f;
+            dot[i] = 0.0f;
+        }
+        for (int64_t at = threadIdx.x * 16; at < pitch; at += kSpan) {
+            float g[P::N];
+            P::unpack(*reinterpret_cast<const uint4*>(d_out + t * pitch + at), g);
+            uint4 v[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                v[i] = load16(make_rsrc(rows + base[i], on[i] ? (uint32_t)pitch : 0u), (uint32_t)at);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (!on[i]) continue;
+                float y[P::N], d[P::N];
+                P::unpack(v[i], y);
+#pragma unroll
+                for (int k = 0; k < P::N; ++k) {
+                    dot[i] = fmaf(g[k], y[k], dot[i]);
+                    d[k] = f[i] * g[k];
+                }
+                *reinterpret_cast<uint4*>(d_rows + base[i] + at) = P::pack(d);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float s = wave_sum(dot[i]);
+            if (lane == 0) part[wave][i] = s;
+        }
+        __syncthreads();
+        if (threadIdx.x < kAtOnce && j0 + (int)threadIdx.x < topk) {
+            float s = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kWavesPerBlock; ++v) s += part[v][threadIdx.x];
+            d_w[t * topk + j0 + threadIdx.x] = s;
+        }
+        __syncthreads();
+    }
+}
+
+dim3 token_grid(int T, int64_t pitch) {
+    return dim3((uint32_t)((pitch + kSpan - 1) / kSpan), (uint32_t)(T < kTokensY ? T : kTokensY),
+                (uint32_t)((T + kTokensY - 1) / kTokensY));
+}
+
+}  // namespace
+
+size_t moe_sort_workspace_bytes(int64_t P, int E) {
+    if (P <= kSortOneMax) return 0;
+    const int64_t chunks = (P + kSortChunk - 1) / kSortChunk;
+    return (size_t)(chunks + 1) * E * 4;
+}
+
+hipError_t launch_moe_sort(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* sorted,
+                           int32_t* positions, void* ws, hipStream_t stream) {
+    int bits = 0;
+    while ((1 << bits) < E) ++bits;
+    if (P <= kSortOneMax) {
+        hipLaunchKernelGGL(moe_sort_one_kernel, dim3(1), dim3(1024), 0, stream, ids, P, E, bits,
+                           offsets, sorted, positions);
+        return hipGetLastError();
+    }
+    const int chunks = (P + kSortChunk - 1) / kSortChunk;
+    int32_t* counts = static_cast<int32_t*>(ws);
+    int32_t* totals = counts + (int64_t)chunks * E;
+    hipLaunchKernelGGL(moe_count_kernel, dim3(chunks), dim3(kBlock), 0, stream, ids, P, E, counts);
+    hipLaunchKernelGGL(moe_scan_kernel, dim3((E + kWave - 1) / kWave), dim3(kWave), 0, stream, counts,
+                       chunks, E, totals);
+    hipLaunchKernelGGL(moe_place_kernel, dim3(chunks), dim3(kBlock), 0, stream, ids, P, E, bits,
+                       counts, totals, offsets, sorted, positions);
+    return hipGetLastError();
+}
+
+int moe_sort_launches(int64_t P) { return P <= kSortOneMax ? 1 : 3; }
+
+hipError_t launch_moe_gather(const void* x, int T, int topk, int64_t pitch, const int32_t* positions,
+                             void* rows, hipStream_t stream) {
+    hipLaunchKernelGGL(moe_gather_kernel, token_grid(T, pitch), dim3(kBlock), 0, stream,
+                       static_cast<const char*>(x), pitch, T, topk, positions,
+                       static_cast<char*>(rows));
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const void* rows, int T, int topk, int64_t pitch, bool f32,
+                              const int32_t* positions, const float* w, const void* r, void* out,
+                              hipStream_t stream) {
+    const auto kernel = f32 ? moe_combine_kernel<true> : moe_combine_kernel<false>;
+    hipLaunchKernelGGL(kernel, token_grid(T, pitch), dim3(kBlock), 0, stream,
+                       static_cast<const char*>(rows), pitch, T, topk, positions, w,
+                       static_cast<const char*>(r), static_cast<char*>(out));
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_grad(const void* d_out, const void* rows, int T, int topk,
+                                   int64_t pitch, bool f32, const int32_t* positions, const float* w,
+                                   void* d_rows, float* d_w, hipStream_t stream) {
+    const auto kernel = f32 ? moe_combine_grad_kernel<true> : moe_combine_grad_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)T), dim3(kBlock), 0, stream,
+                       static_cast<const char*>(d_out), static_cast<const char*>(rows), pitch, T, topk,
+                       positions, w, static_cast<char*>(d_rows), d_w);
+    return hipGetLastError();
+}
+
+}  // namespace sg
