@@ -532,6 +532,8 @@ sg_status grouped_skinny_gemm_fp8(int32_t rows, int32_t x_rows, int32_t E, int32
  *   q = codes of x (skinny_quant_fp8), pairs sorted by expert (skinny_moe_sort)
  *   u = q W_gate_up[e]^T, fp32                          (grouped_skinny_gemm_fp8)
  *   p = codes of silu(u[:, :F]) * u[:, F:]                     (skinny_quant_fp8)
+ *       (for many rows an expert the FP8 instruction's sums; where F % 128 == 0
+ *       the codes then leave the product itself and u is not stored)
  *   y = p W_down[e]^T, bf16                             (grouped_skinny_gemm_fp8)
  *   out[t] = (r[t] +) sum_j topk_weights[t][j] * y          (skinny_moe_combine)
  * x, r, out [T, H] bf16 (r nullable; out may be x's or r's buffer); topk_ids

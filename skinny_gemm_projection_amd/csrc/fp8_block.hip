@@ -18,6 +18,7 @@
 //  * v_mfma_f32_16x16x32_bf16 takes them converted to bf16, exactly, and sums in fp32
 //    (off by 2^-23).  It serves fp32 outputs, and small batches, whose time is the
 //    weight stream's.
+#include "fp8_device.h"
 #include "launch.h"
 #include "tile_device.h"
 
@@ -300,7 +301,19 @@ struct Fp8Tile {
     static_assert(LX * kRowsPerLoad * W == BM && LW * kRowsPerLoad * W == BN, "whole loads a wave");
     static_assert(NB >= 2 && NB <= 4 && W * kWave >= BM, "stage buffers; a scale a thread");
     static_assert(FN * 16 <= kBlockK && kBlockK % (FN * 16) == 0, "a wave's channels in one block");
-    static constexpr int kStage = (BM + BN) * kPieces;  // 16-byte pieces
+    // Two buffers are refilled in parts while they are read; x has two parts, the first
+    // and the second half of every wave's 16-row tiles.
+    static constexpr bool kParts = NB == 2;
+    static constexpr int kXParts = kParts ? 2 : 1;
+    static constexpr int kW = BN * kPieces, kX = BM / kXParts * kPieces;  // 16-byte pieces
+    // Row of x that load l of a wave begins at, and its row in its part's buffer.
+    static __device__ __forceinline__ int x_lds_row(int wave, int l) {
+        return (wave * (LX / kXParts) + l % (LX / kXParts)) * kRowsPerLoad;
+    }
+    static __device__ __forceinline__ int x_row(int wave, int l) {
+        const int at = x_lds_row(wave, l), part = FM * 16 / kXParts;  // rows of a part and wave
+        return at / part * (FM * 16) + l / (LX / kXParts) * part + at % part;
+    }
     static constexpr int kWScales = BN > kBlockK ? BN / kBlockK : 1;
 };
 
@@ -310,16 +323,25 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
     constexpr int BM = T::BM, BN = T::BN, NB = T::NB, FM = T::FM, FN = T::FN, P = T::kPieces;
     constexpr int kRows = T::kRowsPerLoad, kThreads = T::W * kWave;
     constexpr bool kGated = OUT == kTileGated;
-    // An array for each stage buffer: the compiler then knows that a load into one of
-    // them does not delay reads of another.
-    __shared__ uint4 b0[T::kStage], b1[T::kStage], b2[NB > 2 ? T::kStage : 1],
-        b3[NB > 3 ? T::kStage : 1];
-    auto buffer = [&](auto i) -> uint4* {
+    // An array for each part of each stage buffer: the compiler then knows that a load
+    // into one of them does not delay reads of another.
+    __shared__ uint4 w0[T::kW], w1[T::kW], w2[NB > 2 ? T::kW : 1], w3[NB > 3 ? T::kW : 1];
+    __shared__ uint4 p0[T::kX], p1[T::kX], p2[NB > 2 ? T::kX : 1], p3[NB > 3 ? T::kX : 1];
+    __shared__ uint4 q0[T::kParts ? T::kX : 1], q1[T::kParts ? T::kX : 1];
+    auto w_buffer = [&](auto i) -> uint4* {
         constexpr int I = decltype(i)::value % NB;
-        if constexpr (I == 0) return b0;
-        if constexpr (I == 1) return b1;
-        if constexpr (I == 2) return b2;
-        if constexpr (I == 3) return b3;
+        if constexpr (I == 0) return w0;
+        if constexpr (I == 1) return w1;
+        if constexpr (I == 2) return w2;
+        if constexpr (I == 3) return w3;
+    };
+    auto x_buffer = [&](auto i, auto half) -> uint4* {
+        constexpr int I = decltype(i)::value % NB;
+        if constexpr (decltype(half)::value == 1) return I == 0 ? q0 : q1;
+        if constexpr (I == 0) return p0;
+        if constexpr (I == 1) return p1;
+        if constexpr (I == 2) return p2;
+        if constexpr (I == 3) return p3;
     };
     // scales of x, a stage each
     __shared__ float x0[kThreads], x1[kThreads], x2[NB > 2 ? kThreads : 1], x3[NB > 3 ? kThreads : 1];
@@ -397,7 +419,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
     if constexpr (GROUPED) {
 #pragma unroll
         for (int i = 0; i < T::LX; ++i) {
-            const int r = (w * T::LX + i) * kRows + lrow;
+            const int r = T::x_row(w, i) + lrow;
             xrow[i] = gather ? gathered(a, seg, m0 + r, K) : r < here ? (uint32_t)(r * K) : kPastEnd;
             if (xrow[i] != kPastEnd) xrow[i] += kpos;
         }
@@ -407,28 +429,38 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
         srow = r >= BM ? kPastEnd
                        : gather ? gathered(a, seg, m0 + r, 4) : r < here ? (uint32_t)r * 4u : kPastEnd;
     }
-    auto issue = [&](uint4* b, float* s, int k0) {
-        const uint32_t at = k0 < klen ? lbase : kPastEnd;
-#pragma unroll
-        for (int i = 0; i < T::LX; ++i) {
-            const int r = (w * T::LX + i) * kRows;
-            uint32_t off = at + (uint32_t)(r * K + k0);
-            if constexpr (GROUPED)
-                off = k0 < klen && xrow[i] != kPastEnd ? xrow[i] + (uint32_t)k0 : kPastEnd;
-            load_to_lds<kCached>(rx, b + r * P, off);
-        }
-#pragma unroll
-        for (int i = 0; i < T::LW; ++i) {
-            const int r = (w * T::LW + i) * kRows;
-            const bool up = kGated && r % 32 >= 16;
-            const int src = kGated ? r / 32 * 16 + r % 16 : r;
-            load_to_lds<kCached>(up ? ru : rw, b + (BM + r) * P, at + (uint32_t)(src * K + k0));
-        }
+    // One load of the stage that begins at code k0: of a part of x, of W, of the scales of
+    // x.  Past the end they read zeros.
+    constexpr int kHalf = T::LX / T::kXParts;
+    auto load_x = [&](auto i, auto half, int k0, int l) {
+        const int ll = decltype(half)::value * kHalf + l;
+        uint32_t off = (k0 < klen ? lbase : kPastEnd) + (uint32_t)(T::x_row(w, ll) * K + k0);
+        if constexpr (GROUPED)
+            off = k0 < klen && xrow[ll] != kPastEnd ? xrow[ll] + (uint32_t)k0 : kPastEnd;
+        load_to_lds<kCached>(rx, x_buffer(i, half) + T::x_lds_row(w, ll) * P, off);
+    };
+    auto load_w = [&](auto i, int k0, int l) {
+        const int r = (w * T::LW + l) * kRows;
+        const bool up = kGated && r % 32 >= 16;
+        const int src = kGated ? r / 32 * 16 + r % 16 : r;
+        load_to_lds<kCached>(up ? ru : rw, w_buffer(i) + r * P,
+                             (k0 < klen ? lbase : kPastEnd) + (uint32_t)(src * K + k0));
+    };
+    auto load_scales = [&](auto i, int k0) {
         const int kb = min((kbeg + k0) / kBlockK, max(Kb - 1, 0));
         const rsrc_t rs = make_rsrc(a.xs + (int64_t)kb * a.x_rows + base,
                                     kbeg + k0 < kend ? (uint32_t)(gather ? a.x_rows : here) * 4u : 0u);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(s + w * kWave), 4, (int)srow, 0, 0,
-                                                 kCached);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(scales(i) + w * kWave), 4, (int)srow, 0,
+                                                 0, kCached);
+    };
+    const std::integral_constant<int, 0> c0;
+    const std::integral_constant<int, 1> c1;
+    auto load_stage = [&](auto i, int k0) {
+#pragma unroll
+        for (int l = 0; l < T::LW; ++l) load_w(i, k0, l);
+        load_scales(i, k0);
+#pragma unroll
+        for (int l = 0; l < kHalf; ++l) load_x(i, c0, k0, l);
     };
 
     f32x4_t acc[FN][FM];
@@ -437,12 +469,22 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
 #pragma unroll
         for (int j = 0; j < FM; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const int row = lane & 15, grp = lane >> 4, wm = w / T::WN, wn = w % T::WN;
-    const int xat = (wm * FM * 16 + row) * P, wat = (BM + wn * FN * 16 + row) * P;
-    const int p0 = grp ^ (row & 7), p1 = (4 + grp) ^ (row & 7);
-    constexpr int kLoads = T::LX + T::LW + 1, kOut = (NB - 2) * kLoads;
+    constexpr int kTilesPart = FM / T::kXParts;  // 16-row tiles of a part of x
+    const int xat = (wm * kTilesPart * 16 + row) * P, wat = (wn * FN * 16 + row) * P;
+    const int piece0 = grp ^ (row & 7), piece1 = (4 + grp) ^ (row & 7);
     const int n = max(1, (kend - kbeg + kBlockK - 1) / kBlockK);
-    // Stage s: wait until it has landed for every wave, refill the buffer of stage s - 1
-    // (all its reads are done) with stage s + NB - 1, multiply.
+    Frag<WIDE> fw[FN], fx[2];
+    auto read_w = [&](auto i, int c) {
+        const uint4* b = w_buffer(i);
+        fw[c].set(0, b[wat + c * 16 * P + piece0]);
+        fw[c].set(1, b[wat + c * 16 * P + piece1]);
+    };
+    auto read_x = [&](auto i, auto j) {
+        constexpr int J = decltype(j)::value;
+        const uint4* b = x_buffer(i, std::integral_constant<int, J / kTilesPart>{});
+        fx[J % 2].set(0, b[xat + J % kTilesPart * 16 * P + piece0]);
+        fx[J % 2].set(1, b[xat + J % kTilesPart * 16 * P + piece1]);
+    };
     // The products of one 16-row tile of x run while the sums of the tile before (of the
     // stage before, for the first) are scaled and added.
     constexpr int kScales = kGated ? 2 : 1;
@@ -451,54 +493,98 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
     float f[2][kScales] = {};
 #pragma unroll
     for (int c = 0; c < FN; ++c) part[1][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    // Loads return in order, and a wait leaves the last kOut out.
+    // Three or four buffers: stage s begins when its loads have landed for every wave
+    // (those of the stages s + 1 .. s + NB - 2 may be out); then the buffer of stage s - 1,
+    // all of whose reads are done, is refilled with stage s + NB - 1.
+    // Two buffers: a stage's loads are spread over its tiles of x, since waves that issue
+    // all of theirs at once hold each other (and their products) up for as long as the
+    // products take.  So that the late ones still have more than a stage to land, parts of
+    // a buffer are refilled as soon as all waves have read them:
+    //  * from the first tile on, the second half of x of stage s + 1;
+    //  * from the middle, when every wave holds W and the scales in registers and has read
+    //    the first half of x, those of stage s + 2 (there the second half of stage s has to
+    //    be in);
+    //  * at the last tile W, the scales and the first half of stage s + 1 have to be in: its
+    //    W is read behind the last products with this stage's.
+    constexpr int kOut = T::kParts ? 2 * kHalf + T::LW + 1 : (NB - 2) * (T::LX + T::LW + 1);
+    constexpr int kMiddle = kTilesPart - 1;
     auto stage = [&](auto i, int s) {  // s % NB == i
-        constexpr int J = (decltype(i)::value + NB - 1) % NB;
-        const uint4* b = buffer(i);
-        const float* sx = scales(i);
-        wait_and_barrier<kOut>();
-        issue(buffer(std::integral_constant<int, J>{}), scales(std::integral_constant<int, J>{}),
-              (s + NB - 1) * kBlockK);
-        float ws[kScales];
-#pragma unroll
-        for (int c = 0; c < kScales; ++c)
-            ws[c] = sw[kGated ? c : wn * FN * 16 / kBlockK][s];
-        Frag<WIDE> fw[FN], fx[2];
-        auto read_x = [&](auto j) {
-            constexpr int J = decltype(j)::value;
-            fx[J % 2].set(0, b[xat + J * 16 * P + p0]);
-            fx[J % 2].set(1, b[xat + J * 16 * P + p1]);
-        };
-#pragma unroll
-        for (int c = 0; c < FN; ++c) {
-            fw[c].set(0, b[wat + c * 16 * P + p0]);
-            fw[c].set(1, b[wat + c * 16 * P + p1]);
+        const std::integral_constant<int, (decltype(i)::value + NB - 1) % NB> next;
+        const int k_next = (s + NB - 1) * kBlockK;
+        if constexpr (!T::kParts) {
+            wait_and_barrier<kOut>();
+            load_stage(next, k_next);
         }
-        read_x(std::integral_constant<int, 0>{});
+        const float* sx = scales(i);
+        float ws[kScales], xs[FM];
+#pragma unroll
+        for (int c = 0; c < kScales; ++c) ws[c] = sw[kGated ? c : wn * FN * 16 / kBlockK][s];
+#pragma unroll
+        for (int j = 0; j < FM; ++j) xs[j] = sx[(wm * FM + j) * 16 + row];
+        if constexpr (!T::kParts) {
+#pragma unroll
+            for (int c = 0; c < FN; ++c) read_w(i, c);
+            read_x(i, c0);
+        }
         __builtin_amdgcn_sched_barrier(0);
         unrolled<0, FM>([&](auto jc) {
             constexpr int j = decltype(jc)::value, prev = (j + FM - 1) % FM;
-            if constexpr (j + 1 < FM) read_x(std::integral_constant<int, j + 1>{});
-            const float xs = sx[(wm * FM + j) * 16 + row];
+            constexpr bool kLast = T::kParts && j == FM - 1;
+            if constexpr (T::kParts) {
+                const int k2 = (s + 2) * kBlockK;
+                if constexpr (j == kMiddle || kLast) wait_and_barrier<kOut>();
+                if constexpr (j < kHalf) load_x(next, c1, k_next, j);
+                if constexpr (j >= kMiddle && !kLast) {
+                    // W, the scales and the first half of x over the tiles left but the last
+                    constexpr int kAll = T::LW + 1 + kHalf, kOver = FM - 1 - kMiddle, at = j - kMiddle;
+                    unrolled<kAll * at / kOver, kAll*(at + 1) / kOver>([&](auto lc) {
+                        constexpr int l = decltype(lc)::value;
+                        if constexpr (l < T::LW)
+                            load_w(i, k2, l);
+                        else if constexpr (l == T::LW)
+                            load_scales(i, k2);
+                        else
+                            load_x(i, c0, k2, l - T::LW - 1);
+                    });
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (j + 1 < FM)
+                read_x(i, std::integral_constant<int, j + 1>{});
+            else if constexpr (kLast)
+                read_x(next, c0);
 #pragma unroll
             for (int c = 0; c < FN; ++c) {
                 part[j % 2][c] = block_sum(fw[c], fx[j % 2]);
+                if constexpr (kLast) read_w(next, c);
                 add_scaled(acc[c][prev], part[(j + 1) % 2][c], f[(j + 1) % 2][c % kScales]);
                 asm volatile("" : "+v"(acc[c][prev]));  // added here, not behind the stage
             }
 #pragma unroll
-            for (int c = 0; c < kScales; ++c) f[j % 2][c] = xs * ws[c];
-            if constexpr (j + 1 < FM) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);  // LDS reads
+            for (int c = 0; c < kScales; ++c) f[j % 2][c] = xs[j] * ws[c];
+            if constexpr (j + 1 < FM || kLast) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
 #pragma unroll
             for (int c = 0; c < FN; ++c) {
                 __builtin_amdgcn_sched_group_barrier(0x8, WIDE ? 4 : 1, 0);  // matrix instructions
-                __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);             // vector arithmetic
+                if constexpr (kLast) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);  // vector arithmetic
             }
             __builtin_amdgcn_sched_barrier(0);  // reads stay one tile ahead: more would not fit
         });
     };
-    unrolled<0, NB - 1>([&](auto i) {
-        issue(buffer(i), scales(i), decltype(i)::value * kBlockK);
-    });
+    load_stage(c0, 0);
+    if constexpr (T::kParts) {
+#pragma unroll
+        for (int l = 0; l < kHalf; ++l) load_x(c0, c1, 0, l);
+        load_stage(c1, kBlockK);
+        wait_and_barrier<kOut>();
+#pragma unroll
+        for (int c = 0; c < FN; ++c) read_w(c0, c);
+        read_x(c0, c0);
+    } else {
+        unrolled<1, NB - 1>([&](auto i) { load_stage(i, decltype(i)::value * kBlockK); });
+    }
     int s = 0;
     for (; s + NB <= n; s += NB)
         unrolled<0, NB>([&](auto i) { stage(i, s + decltype(i)::value); });
@@ -517,7 +603,42 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
             for (int j = 0; j < FM; ++j)
                 if ((wm * FM + j) * 16 < here)
                     reinterpret_cast<f32x4_t*>(out)[((w * FN + i) * FM + j) * kWave + lane] = acc[i][j];
-    } else if constexpr (OUT == kTileFinal) {
+    } else if constexpr (OUT == kTileGated) {
+        // silu(gate) * up of the tile's 128 outputs, which are one block of every row: the
+        // largest of a row meets in LDS, then each lane writes the codes of what it holds.
+        static_assert(BC == kBlockK && FN % 2 == 0, "a block of outputs a tile, gate and up beside");
+        __shared__ uint32_t largest[T::WN][BM];
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            uint32_t amax = 0;
+#pragma unroll
+            for (int c = 0; c < FN; c += 2)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    acc[c][j][v] = gated_product(acc[c][j][v], acc[c + 1][j][v]);
+                    amax = max(amax, as_u(acc[c][j][v]) & 0x7fffffffu);
+                }
+            amax = max(amax, (uint32_t)__shfl_xor((int)amax, 16, kWave));
+            amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32, kWave));
+            if (grp == 0) largest[wn][(wm * FM + j) * 16 + row] = amax;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int ml = (wm * FM + j) * 16 + row;
+            if (ml >= here) continue;
+            uint32_t amax = 0;
+#pragma unroll
+            for (int o = 0; o < T::WN; ++o) amax = max(amax, largest[o][ml]);
+            const BlockScale s = block_scale(amax);
+            const int64_t m = seg.begin + m0 + ml;
+            if (wn == 0 && grp == 0) a.scales[(int64_t)(n0 / kBlockK) * a.M + m] = s.unit;
+#pragma unroll
+            for (int c = 0; c < FN; c += 2)
+                *reinterpret_cast<uint32_t*>(a.codes + m * N + n0 + (wn * FN + c) * 8 + grp * 4) =
+                    codes4(acc[c][j][0], acc[c][j][1], acc[c][j][2], acc[c][j][3], s);
+        }
+    } else {
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
             const int ml = (wm * FM + j) * 16 + row;
@@ -569,11 +690,12 @@ __global__ __launch_bounds__(kBlock) void fp8_reduce_kernel(const float* __restr
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile variants, BM x BN: 256 x 256, 128 x 256, 128 x 128, 64 x 128.
+// Tile variants, BM x BN: 256 x 256, 128 x 256, 128 x 128, 64 x 128, 64 x 256.
 typedef Fp8Tile<2, 4, 8, 4, 2> Tile256;
 typedef Fp8Tile<2, 4, 4, 4, 3> Tile128w;
 typedef Fp8Tile<2, 4, 4, 2, 4> Tile128;
 typedef Fp8Tile<2, 2, 2, 4, 3> Tile64;
+typedef Fp8Tile<2, 4, 2, 4, 3> Tile64w;
 
 template <class F>
 void with_tile(int v, F f) {
@@ -581,7 +703,8 @@ void with_tile(int v, F f) {
         case 0: f(Tile256{}); break;
         case 1: f(Tile128w{}); break;
         case 2: f(Tile128{}); break;
-        default: f(Tile64{}); break;
+        case 3: f(Tile64{}); break;
+        default: f(Tile64w{}); break;
     }
 }
 
@@ -595,8 +718,9 @@ struct TileCost {
 constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.0, 9.9},
                                {128, 256, 1, 8, 7.2, 6.2},
                                {128, 128, 1, 8, 4.1, 3.9},
-                               {64, 128, 2, 8, 6.4, 3.6}};
-constexpr int kTileVariants = 4;
+                               {64, 128, 2, 8, 6.4, 3.6},
+                               {64, 256, 1, 8, 5.0, 4.5}};
+constexpr int kTileVariants = 5;
 constexpr int kCus = 256;
 constexpr int kTeamMaxM = 64;
 
@@ -628,10 +752,10 @@ int64_t most_tiles(int M, int E, int N) {
     return ((int64_t)M / T::BM + (E < M ? E : M)) * ceil_div(N, T::BN);
 }
 
-template <class T, bool WIDE>
+template <class T, int OUT, bool WIDE>
 void launch_grouped_tiles(const Fp8Product& a, hipStream_t stream) {
-    const int64_t tiles = most_tiles<T>(a.M, a.E, a.N);
-    hipLaunchKernelGGL((fp8_tile_kernel<T, kTileFinal, true, WIDE>),
+    const int64_t tiles = most_tiles<T>(a.M, a.E, OUT == kTileGated ? 2 * a.N : a.N);
+    hipLaunchKernelGGL((fp8_tile_kernel<T, OUT, true, WIDE>),
                        dim3((uint32_t)(ceil_div(tiles, kXcds) * kXcds)), dim3(T::W * kWave), 0, stream, a,
                        0, 0, 0, a.K, nullptr);
 }
@@ -655,7 +779,7 @@ void launch_team(int mt, const Fp8Product& a, hipStream_t stream) {
 }  // namespace
 
 Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide) {
-    if (M <= kTeamMaxM) return Fp8BlockPlan{Fp8BlockPlan::kTeam, (M + 15) / 16, 0, 1, K, 0};
+    if (M <= kTeamMaxM) return Fp8BlockPlan{Fp8BlockPlan::kTeam, (M + 15) / 16, 0, 1, K, 0, true};
     Fp8BlockPlan best{};
     double least = 1e30;
     for (int v = wide ? 1 : 0; v < kTileVariants; ++v) {
@@ -670,7 +794,7 @@ Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide) {
             if (S > 1) est += 3.0 + 8.0 * S * M * N / 4.0e6;
             if (est < least && ws <= ((size_t)1 << 30)) {
                 least = est;
-                best = Fp8BlockPlan{Fp8BlockPlan::kTile, 0, v, S, kc, ws};
+                best = Fp8BlockPlan{Fp8BlockPlan::kTile, 0, v, S, kc, ws, wide};
             }
         }
     }
@@ -679,9 +803,16 @@ Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide) {
 
 Fp8BlockPlan fp8_grouped_plan(int M, int E, int N, int K, bool wide) {
     const int64_t rows = M / (E < M ? E : M);  // an expert's, on average
-    if (rows <= 24)
-        return Fp8BlockPlan{Fp8BlockPlan::kTeam, rows <= 4 ? 1 : 2, 0, 1, K, 0};
-    return Fp8BlockPlan{Fp8BlockPlan::kTile, 0, rows <= 64 ? 3 : rows <= 160 || wide ? 1 : 0, 1, K, 0};
+    if (rows <= 24) return Fp8BlockPlan{Fp8BlockPlan::kTeam, rows <= 4 ? 1 : 2, 0, 1, K, 0, true};
+    const int tile = rows <= 64 ? 4 : rows <= 160 || wide ? 1 : 0;
+    return Fp8BlockPlan{Fp8BlockPlan::kTile, 0, tile, 1, K, 0, wide};
+}
+
+bool fp8_gated_ok(const Fp8BlockPlan& p, int F) {
+    bool ok = false;
+    if (p.kind == Fp8BlockPlan::kTile && !p.wide)
+        with_tile(p.tile, [&](auto shape) { ok = decltype(shape)::BN == 2 * kBlockK; });
+    return ok && F % kBlockK == 0;
 }
 
 bool fp8_grouped_fits(const Fp8BlockPlan& p, int M, int E, int N) {
@@ -698,7 +829,6 @@ hipError_t launch_fp8_block(const Fp8BlockPlan& p, const Fp8Product& product, vo
                             hipStream_t stream) {
     Fp8Product a = product;
     a.ld = a.N;
-    const bool wide = a.y_f32 != nullptr;
     if (p.kind == Fp8BlockPlan::kTeam) {
         if (a.offsets)
             launch_team<true>(p.mt, a, stream);
@@ -708,17 +838,20 @@ hipError_t launch_fp8_block(const Fp8BlockPlan& p, const Fp8Product& product, vo
     }
     with_tile(p.tile, [&](auto shape) {
         typedef decltype(shape) T;
-        if (wide) {
+        const int group = kTiles[p.tile].group;
+        if (p.wide) {
             if constexpr (T::FM * T::FN <= 16) {
                 if (a.offsets)
-                    launch_grouped_tiles<T, true>(a, stream);
+                    launch_grouped_tiles<T, kTileFinal, true>(a, stream);
                 else
-                    launch_plain<T, true>(a, p.S, p.kc, kTiles[p.tile].group, ws, stream);
+                    launch_plain<T, true>(a, p.S, p.kc, group, ws, stream);
             }
+        } else if (a.codes) {
+            if constexpr (T::BN == 2 * kBlockK) launch_grouped_tiles<T, kTileGated, false>(a, stream);
         } else if (a.offsets) {
-            launch_grouped_tiles<T, false>(a, stream);
+            launch_grouped_tiles<T, kTileFinal, false>(a, stream);
         } else {
-            launch_plain<T, false>(a, p.S, p.kc, kTiles[p.tile].group, ws, stream);
+            launch_plain<T, false>(a, p.S, p.kc, group, ws, stream);
         }
     });
     return hipGetLastError();

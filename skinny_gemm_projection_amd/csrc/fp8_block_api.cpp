@@ -69,6 +69,7 @@ sg_status product(const sg::Fp8BlockPlan& plan, const sg::Fp8Product& a, void* w
 struct StepLayout {
     size_t q, sq, offsets, sorted, positions, sort, u, p, sp, y, total;
     sg::Fp8BlockPlan up, down;
+    bool gated;  // the first product gives the gated product's codes itself
 };
 
 bool step_layout(int32_t T, int32_t topk, int32_t E, int32_t H, int32_t F, StepLayout* L) {
@@ -83,7 +84,9 @@ bool step_layout(int32_t T, int32_t topk, int32_t E, int32_t H, int32_t F, StepL
     };
     const size_t P = (size_t)T * topk, t = (size_t)T;
     const int rows = P > 0 ? (int)P : 1;
-    L->up = sg::fp8_grouped_plan(rows, E, 2 * F, H, true);
+    // what follows is rounded to 4 bits: the FP8 instruction's sums do
+    L->up = sg::fp8_grouped_plan(rows, E, 2 * F, H, false);
+    L->gated = sg::fp8_gated_ok(L->up, F);
     L->down = sg::fp8_grouped_plan(rows, E, H, F, false);
     L->q = take(t * H);
     L->sq = take(t * ((H + 127) / 128) * 4);
@@ -91,7 +94,7 @@ bool step_layout(int32_t T, int32_t topk, int32_t E, int32_t H, int32_t F, StepL
     L->sorted = take(P * 4);
     L->positions = take(P * 4);
     L->sort = take(sg::moe_sort_workspace_bytes((int64_t)P, E));
-    L->u = take(P * F * 8);
+    L->u = take(L->gated ? 0 : P * F * 8);
     L->p = take(P * F);
     L->sp = take(P * ((F + 127) / 128) * 4);
     L->y = take(P * H * 2);
@@ -282,8 +285,9 @@ sg_status skinny_moe_fp8_step(const sg_moe_fp8_step* a, void* workspace, size_t 
     if ((st = quant(T, H, a->x, false, false, q, sq, hs)) != SG_OK) return st;
     sg::Fp8Product up{q, sq, a->W_gate_up, a->gate_up_scales, P, 2 * F, H, T, u, nullptr, nullptr};
     up.offsets = offsets, up.E = E, up.pairs = sorted, up.topk = topk;
+    if (L.gated) up.N = F, up.y_f32 = nullptr, up.codes = p, up.scales = sp;
     if ((st = product(L.up, up, nullptr, hs)) != SG_OK) return st;
-    if ((st = quant(P, F, u, true, true, p, sp, hs)) != SG_OK) return st;
+    if (!L.gated && (st = quant(P, F, u, true, true, p, sp, hs)) != SG_OK) return st;
     // the rows of y are bf16: one rounding each before the weighted sum
     sg::Fp8Product down{p, sp, a->W_down, a->down_scales, P, H, F, P, nullptr, y, nullptr};
     down.offsets = offsets, down.E = E;

@@ -257,11 +257,14 @@ struct Fp8BlockPlan {
     int mt;                // team kernel: 16-row tiles of x
     int tile, S, kc;       // tile kernel: variant, K splits, codes a split
     size_t workspace;      // bytes of fp32 partial sums (S > 1)
+    bool wide;             // the bf16 instruction: sums at fp32's precision
 };
-// wide: fp32 outputs are wanted.
 Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide);
 // experts: M pairs over E experts
 Fp8BlockPlan fp8_grouped_plan(int M, int E, int N, int K, bool wide);
+// Whether a grouped product of 2F gate and up rows by this plan can give the gated
+// product's codes itself (Fp8Product::codes, N = F).
+bool fp8_gated_ok(const Fp8BlockPlan& p, int F);
 bool fp8_grouped_fits(const Fp8BlockPlan& p, int M, int E, int N);  // in one launch's limits
 hipError_t launch_fp8_block(const Fp8BlockPlan& p, const Fp8Product& a, void* ws, hipStream_t stream);
 

@@ -8,18 +8,12 @@
 // alone, and halfway cases are real ones.  (With scale = max |v| / 448 the rounding
 // of the quotient decides them; rows of bf16 have many.)  A floating-point code
 // loses nothing by the coarser scale but up to one binade below its normal range.
-// The scale is read off the bits of the maximum: its exponent, less 8, plus 1
-// where its mantissa is past 1.75 (448 = 1.75 * 2^8).
-#include <math.h>
-
-#include "int8_device.h"
+#include "fp8_device.h"
 #include "launch.h"
 
 namespace sg {
 
 namespace {
-
-constexpr uint32_t kInfBits = 0x7f800000u;
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
@@ -77,18 +71,12 @@ __global__ __launch_bounds__(kBlock) void quant_fp8_kernel(const char* __restric
         amax = dpp_umax<0x4E>(amax);   // quad_perm [2,3,0,1]
         amax = dpp_umax<0x141>(amax);  // row_half_mirror
         amax = dpp_umax<0x140>(amax);  // row_mirror
-        const bool bad = amax >= kInfBits;
-        const int e = max((int)((amax + 0x1fffffu) >> 23) - 8, 1);
-        const float inv = as_f((uint32_t)(254 - e) << 23);
-        unit[i] = bad ? __builtin_nanf("") : as_f((uint32_t)e << 23);
-        int lo = 0, hi = 0;
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[i][0] * inv, t[i][1] * inv, lo, false);
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[i][2] * inv, t[i][3] * inv, lo, true);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[i][4] * inv, t[i][5] * inv, hi, false);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[i][6] * inv, t[i][7] * inv, hi, true);
+        const BlockScale s = block_scale(amax);
+        unit[i] = s.unit;
         if (piece * 8 < K && r0 + i < M)
             *reinterpret_cast<uint2*>(codes + (r0 + i) * K + piece * 8) =
-                bad ? make_uint2(0, 0) : make_uint2((uint32_t)lo, (uint32_t)hi);
+                make_uint2(codes4(t[i][0], t[i][1], t[i][2], t[i][3], s),
+                           codes4(t[i][4], t[i][5], t[i][6], t[i][7], s));
     }
     const int b = span * 4 + (lane >> 4);
     if ((lane & 15) == 0 && b * 128 < K) {

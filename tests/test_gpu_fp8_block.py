@@ -371,7 +371,8 @@ def step_reference(x, ids, w, wgu, sgu, wd, sd, r, E):
 
 STEP = [(1, 1, 1, 16, 16, 1), (1, 8, 16, 144, 128, 16), (4, 8, 40, 272, 144, 53), (9, 2, 3, 128, 272, 4),
         (33, 4, 8, 528, 256, 8), (130, 2, 3, 256, 128, 3), (70, 6, 12, 400, 144, 12),
-        (300, 1, 2, 144, 272, 3), (260, 3, 2, 256, 256, 4), (515, 2, 3, 128, 384, 3)]
+        (300, 1, 2, 144, 272, 3), (260, 3, 2, 256, 256, 4), (515, 2, 3, 128, 384, 3),
+        (100, 4, 10, 272, 256, 12)]
 
 
 def step_inputs(T, topk, E, H, F, total, seed=1):
