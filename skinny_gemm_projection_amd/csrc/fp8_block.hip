@@ -301,8 +301,8 @@ struct Fp8Tile {
     static_assert(LX * kRowsPerLoad * W == BM && LW * kRowsPerLoad * W == BN, "whole loads a wave");
     static_assert(NB >= 2 && NB <= 4 && W * kWave >= BM, "stage buffers; a scale a thread");
     static_assert(FN * 16 <= kBlockK && kBlockK % (FN * 16) == 0, "a wave's channels in one block");
-    // Two buffers are refilled in parts while they are read; x has two parts, the first
-    // and the second half of every wave's 16-row tiles.
+    // Two buffers are refilled in parts while they are read; x has two parts, its first
+    // and its second half: the waves take its 16-row tiles in turn.
     static constexpr bool kParts = NB == 2;
     static constexpr int kXParts = kParts ? 2 : 1;
     static constexpr int kW = BN * kPieces, kX = BM / kXParts * kPieces;  // 16-byte pieces
@@ -311,9 +311,10 @@ struct Fp8Tile {
         return (wave * (LX / kXParts) + l % (LX / kXParts)) * kRowsPerLoad;
     }
     static __device__ __forceinline__ int x_row(int wave, int l) {
-        const int at = x_lds_row(wave, l), part = FM * 16 / kXParts;  // rows of a part and wave
-        return at / part * (FM * 16) + l / (LX / kXParts) * part + at % part;
+        return l / (LX / kXParts) * (BM / kXParts) + x_lds_row(wave, l);
     }
+    // First row of a wave's tile j.
+    static __device__ __forceinline__ int tile_row(int wm, int j) { return (j * WM + wm) * 16; }
     static constexpr int kWScales = BN > kBlockK ? BN / kBlockK : 1;
 };
 
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
     constexpr int BC = kGated ? BN / 2 : BN;
     const int nn = (N + BC - 1) / BC;
     Segment seg{0, 0, a.M};
-    int t, m0, n0;
+    int t, m0, n0, high = BM;
     if constexpr (GROUPED) {
         int v, first;
         seg = find_unit<kThreads>(
@@ -372,9 +373,11 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
             },
             &v, &first);
         if (seg.count == 0) return;
-        // tiles of an expert: down its rows before the next tile of its W
-        const int in = t - first * nn, mt = (seg.count + BM - 1) / BM;
-        m0 = in % mt * BM, n0 = in / mt * BC;
+        // tiles of an expert: down its rows before the next tile of its W, all as high as
+        // the waves' turns allow (a tile's time goes by its rows)
+        const int in = t - first * nn, mt = (seg.count + BM - 1) / BM, step = 16 * T::WM;
+        high = ((seg.count + mt - 1) / mt + step - 1) / step * step;
+        m0 = in % mt * high, n0 = in / mt * BC;
     } else {
         // Workgroups reach the 8 XCDs in turn: each XCD takes a run of consecutive
         // tiles, and a run goes down `group` tiles of x before the next tile of W, so
@@ -387,7 +390,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
         m0 = (first + in % rows) * BM, n0 = in / rows * BC;
     }
     const int kbeg = blockIdx.y * kc, kend = min(K, kbeg + kc);
-    const int here = min(BM, seg.count - m0);
+    const int here = min(high, seg.count - m0);
     const bool gather = GROUPED && a.pairs;
     const int64_t base = gather ? 0 : seg.begin + m0;  // row of x of the tile's first
     const int64_t wbase = (int64_t)seg.e * (kGated ? 2 : 1) * N;  // row of W
@@ -470,7 +473,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
         for (int j = 0; j < FM; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const int row = lane & 15, grp = lane >> 4, wm = w / T::WN, wn = w % T::WN;
     constexpr int kTilesPart = FM / T::kXParts;  // 16-row tiles of a part of x
-    const int xat = (wm * kTilesPart * 16 + row) * P, wat = (wn * FN * 16 + row) * P;
+    const int xat = (T::tile_row(wm, 0) + row) * P, wat = (wn * FN * 16 + row) * P;
     const int piece0 = grp ^ (row & 7), piece1 = (4 + grp) ^ (row & 7);
     const int n = max(1, (kend - kbeg + kBlockK - 1) / kBlockK);
     Frag<WIDE> fw[FN], fx[2];
@@ -482,8 +485,9 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
     auto read_x = [&](auto i, auto j) {
         constexpr int J = decltype(j)::value;
         const uint4* b = x_buffer(i, std::integral_constant<int, J / kTilesPart>{});
-        fx[J % 2].set(0, b[xat + J % kTilesPart * 16 * P + piece0]);
-        fx[J % 2].set(1, b[xat + J % kTilesPart * 16 * P + piece1]);
+        constexpr int kAt = J % kTilesPart * T::WM * 16 * P;
+        fx[J % 2].set(0, b[xat + kAt + piece0]);
+        fx[J % 2].set(1, b[xat + kAt + piece1]);
     };
     // The products of one 16-row tile of x run while the sums of the tile before (of the
     // stage before, for the first) are scaled and added.
@@ -507,92 +511,118 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
     //    be in);
     //  * at the last tile W, the scales and the first half of stage s + 1 have to be in: its
     //    W is read behind the last products with this stage's.
-    constexpr int kOut = T::kParts ? 2 * kHalf + T::LW + 1 : (NB - 2) * (T::LX + T::LW + 1);
-    constexpr int kMiddle = kTilesPart - 1;
-    auto stage = [&](auto i, int s) {  // s % NB == i
-        const std::integral_constant<int, (decltype(i)::value + NB - 1) % NB> next;
-        const int k_next = (s + NB - 1) * kBlockK;
-        if constexpr (!T::kParts) {
-            wait_and_barrier<kOut>();
-            load_stage(next, k_next);
-        }
-        const float* sx = scales(i);
-        float ws[kScales], xs[FM];
+    // (Where no wave needs the second half, it is not loaded, and the loads of stage s + 2
+    // follow the wait at the last tile.)
+    // act: tiles of x that the waves take, fewer than FM where a tile of rows is not full.
+    auto run = [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        static_assert(ACT % 2 == 0, "the tiles of x alternate between two sets of sums");
+        constexpr bool kSecond = T::kParts && ACT > kTilesPart;
+        constexpr int kOut = kSecond ? 2 * kHalf + T::LW + 1 : T::kParts ? 0 : (NB - 2) * (T::LX + T::LW + 1);
+        constexpr int kMiddle = kSecond ? kTilesPart - 1 : ACT - 1;
+        auto stage = [&](auto i, int s) {  // s % NB == i
+            const std::integral_constant<int, (decltype(i)::value + NB - 1) % NB> next;
+            const int k_next = (s + NB - 1) * kBlockK;
+            if constexpr (!T::kParts) {
+                wait_and_barrier<kOut>();
+                load_stage(next, k_next);
+            }
+            const float* sx = scales(i);
+            float ws[kScales], xs[ACT];
 #pragma unroll
-        for (int c = 0; c < kScales; ++c) ws[c] = sw[kGated ? c : wn * FN * 16 / kBlockK][s];
+            for (int c = 0; c < kScales; ++c) ws[c] = sw[kGated ? c : wn * FN * 16 / kBlockK][s];
 #pragma unroll
-        for (int j = 0; j < FM; ++j) xs[j] = sx[(wm * FM + j) * 16 + row];
-        if constexpr (!T::kParts) {
+            for (int j = 0; j < ACT; ++j) xs[j] = sx[T::tile_row(wm, j) + row];
+            if constexpr (!T::kParts) {
 #pragma unroll
-            for (int c = 0; c < FN; ++c) read_w(i, c);
-            read_x(i, c0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        unrolled<0, FM>([&](auto jc) {
-            constexpr int j = decltype(jc)::value, prev = (j + FM - 1) % FM;
-            constexpr bool kLast = T::kParts && j == FM - 1;
-            if constexpr (T::kParts) {
-                const int k2 = (s + 2) * kBlockK;
-                if constexpr (j == kMiddle || kLast) wait_and_barrier<kOut>();
-                if constexpr (j < kHalf) load_x(next, c1, k_next, j);
-                if constexpr (j >= kMiddle && !kLast) {
-                    // W, the scales and the first half of x over the tiles left but the last
-                    constexpr int kAll = T::LW + 1 + kHalf, kOver = FM - 1 - kMiddle, at = j - kMiddle;
-                    unrolled<kAll * at / kOver, kAll*(at + 1) / kOver>([&](auto lc) {
-                        constexpr int l = decltype(lc)::value;
-                        if constexpr (l < T::LW)
-                            load_w(i, k2, l);
-                        else if constexpr (l == T::LW)
-                            load_scales(i, k2);
-                        else
-                            load_x(i, c0, k2, l - T::LW - 1);
-                    });
+                for (int c = 0; c < FN; ++c) read_w(i, c);
+                read_x(i, c0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            unrolled<0, ACT>([&](auto jc) {
+                constexpr int j = decltype(jc)::value, prev = (j + ACT - 1) % ACT;
+                constexpr bool kLast = T::kParts && j == ACT - 1;
+                if constexpr (T::kParts) {
+                    const int k2 = (s + 2) * kBlockK;
+                    if constexpr (j == kMiddle || kLast) wait_and_barrier<kOut>();
+                    if constexpr (kSecond && j < kHalf) load_x(next, c1, k_next, j);
+                    if constexpr (j >= kMiddle && !(kSecond && kLast)) {
+                        // W, the scales and the first half of x over the tiles left but the last
+                        constexpr int kAll = T::LW + 1 + kHalf, kOver = kSecond ? ACT - 1 - kMiddle : 1;
+                        constexpr int kAt = j - kMiddle;
+                        unrolled<kAll * kAt / kOver, kAll*(kAt + 1) / kOver>([&](auto lc) {
+                            constexpr int l = decltype(lc)::value;
+                            if constexpr (l < T::LW)
+                                load_w(i, k2, l);
+                            else if constexpr (l == T::LW)
+                                load_scales(i, k2);
+                            else
+                                load_x(i, c0, k2, l - T::LW - 1);
+                        });
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            if constexpr (j + 1 < FM)
-                read_x(i, std::integral_constant<int, j + 1>{});
-            else if constexpr (kLast)
-                read_x(next, c0);
+                if constexpr (j + 1 < ACT)
+                    read_x(i, std::integral_constant<int, j + 1>{});
+                else if constexpr (kLast)
+                    read_x(next, c0);
+                // ahead of the other wave of the SIMD while it loads: 403 -> 396 us at 8192 x 8192 x 7168
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int c = 0; c < FN; ++c) {
-                part[j % 2][c] = block_sum(fw[c], fx[j % 2]);
-                if constexpr (kLast) read_w(next, c);
-                add_scaled(acc[c][prev], part[(j + 1) % 2][c], f[(j + 1) % 2][c % kScales]);
-                asm volatile("" : "+v"(acc[c][prev]));  // added here, not behind the stage
-            }
+                for (int c = 0; c < FN; ++c) {
+                    part[j % 2][c] = block_sum(fw[c], fx[j % 2]);
+                    if constexpr (kLast) read_w(next, c);
+                    add_scaled(acc[c][prev], part[(j + 1) % 2][c], f[(j + 1) % 2][c % kScales]);
+                    asm volatile("" : "+v"(acc[c][prev]));  // added here, not behind the stage
+                }
 #pragma unroll
-            for (int c = 0; c < kScales; ++c) f[j % 2][c] = xs[j] * ws[c];
-            if constexpr (j + 1 < FM || kLast) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+                for (int c = 0; c < kScales; ++c) f[j % 2][c] = xs[j] * ws[c];
+                if constexpr (j + 1 < ACT || kLast) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
 #pragma unroll
-            for (int c = 0; c < FN; ++c) {
-                __builtin_amdgcn_sched_group_barrier(0x8, WIDE ? 4 : 1, 0);  // matrix instructions
-                if constexpr (kLast) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-                __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);  // vector arithmetic
+                for (int c = 0; c < FN; ++c) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, WIDE ? 4 : 1, 0);  // matrix instructions
+                    if constexpr (kLast) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);  // vector arithmetic
+                }
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);  // reads stay one tile ahead: more would not fit
+            });
+        };
+        load_stage(c0, 0);
+        if constexpr (T::kParts) {
+            if constexpr (kSecond) {
+#pragma unroll
+                for (int l = 0; l < kHalf; ++l) load_x(c0, c1, 0, l);
             }
-            __builtin_amdgcn_sched_barrier(0);  // reads stay one tile ahead: more would not fit
+            load_stage(c1, kBlockK);
+            wait_and_barrier<kSecond ? kOut : T::LW + 1 + kHalf>();
+#pragma unroll
+            for (int c = 0; c < FN; ++c) read_w(c0, c);
+            read_x(c0, c0);
+        } else {
+            unrolled<1, NB - 1>([&](auto i) { load_stage(i, decltype(i)::value * kBlockK); });
+        }
+        int s = 0;
+        for (; s + NB <= n; s += NB)
+            unrolled<0, NB>([&](auto i) { stage(i, s + decltype(i)::value); });
+        unrolled<0, NB - 1>([&](auto i) {
+            if (s + decltype(i)::value < n) stage(i, s + decltype(i)::value);
         });
+#pragma unroll
+        for (int c = 0; c < FN; ++c) add_scaled(acc[c][ACT - 1], part[1][c], f[1][c % kScales]);
     };
-    load_stage(c0, 0);
-    if constexpr (T::kParts) {
-#pragma unroll
-        for (int l = 0; l < kHalf; ++l) load_x(c0, c1, 0, l);
-        load_stage(c1, kBlockK);
-        wait_and_barrier<kOut>();
-#pragma unroll
-        for (int c = 0; c < FN; ++c) read_w(c0, c);
-        read_x(c0, c0);
+    const std::integral_constant<int, FM> all;
+    if constexpr (!GROUPED || FM < 4) {
+        run(all);
     } else {
-        unrolled<1, NB - 1>([&](auto i) { load_stage(i, decltype(i)::value * kBlockK); });
+        constexpr int kStep = 16 * T::WM;
+        if (here <= FM / 2 * kStep)
+            run(std::integral_constant<int, FM / 2>{});
+        else if (FM >= 8 && here <= FM / 4 * 3 * kStep)
+            run(std::integral_constant<int, FM / 4 * 3 / 2 * 2>{});
+        else
+            run(all);
     }
-    int s = 0;
-    for (; s + NB <= n; s += NB)
-        unrolled<0, NB>([&](auto i) { stage(i, s + decltype(i)::value); });
-    unrolled<0, NB - 1>([&](auto i) {
-        if (s + decltype(i)::value < n) stage(i, s + decltype(i)::value);
-    });
-#pragma unroll
-    for (int c = 0; c < FN; ++c) add_scaled(acc[c][FM - 1], part[1][c], f[1][c % kScales]);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may outlive the workgroup's LDS
 
     if constexpr (OUT == kTilePartial) {
@@ -601,7 +631,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int j = 0; j < FM; ++j)
-                if ((wm * FM + j) * 16 < here)
+                if (T::tile_row(wm, j) < here)
                     reinterpret_cast<f32x4_t*>(out)[((w * FN + i) * FM + j) * kWave + lane] = acc[i][j];
     } else if constexpr (OUT == kTileGated) {
         // silu(gate) * up of the tile's 128 outputs, which are one block of every row: the
@@ -620,12 +650,12 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
                 }
             amax = max(amax, (uint32_t)__shfl_xor((int)amax, 16, kWave));
             amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32, kWave));
-            if (grp == 0) largest[wn][(wm * FM + j) * 16 + row] = amax;
+            if (grp == 0) largest[wn][T::tile_row(wm, j) + row] = amax;
         }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
-            const int ml = (wm * FM + j) * 16 + row;
+            const int ml = T::tile_row(wm, j) + row;
             if (ml >= here) continue;
             uint32_t amax = 0;
 #pragma unroll
@@ -641,7 +671,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
     } else {
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
-            const int ml = (wm * FM + j) * 16 + row;
+            const int ml = T::tile_row(wm, j) + row;
             if (ml >= here) continue;
 #pragma unroll
             for (int i = 0; i < FN; ++i) {
@@ -670,7 +700,7 @@ __global__ __launch_bounds__(kBlock) void fp8_reduce_kernel(const float* __restr
     const int rows = min(group, nm - first);
     const int m0 = (first + in % rows) * BM, n0 = in / rows * BN;
     const int w = f / (FM * FN), i = f / FM % FN, j = f % FM;
-    const int m = m0 + ((w / T::WN) * FM + j) * 16 + (lane & 15);
+    const int m = m0 + T::tile_row(w / T::WN, j) + (lane & 15);
     const int n = n0 + ((w % T::WN) * FN + i) * 16 + (lane >> 4) * 4;
     if (m >= a.M || n >= a.N) return;
     const f32x4_t* p =
