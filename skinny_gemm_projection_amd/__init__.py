@@ -585,7 +585,7 @@ def skinny_gemm_fp8_block(x_codes: torch.Tensor, x_scales: torch.Tensor, W_codes
     [ceil(N/128), ceil(K/128)]; any M up to 2^20.  Writes y_f32 and/or y_bf16 [M, N]; with r (bf16
     [M, N]) the fused residual y = r + product (y_bf16 may be r).  Allocates y_f32 when no output
     is given, and the workspace when one is needed and none is given; returns the outputs.
-    (y_bf16 alone, past 64 rows, takes the FP8 matrix instruction: see the header on its sums.)"""
+    (y_bf16 alone, past 32 rows, takes the FP8 matrix instruction: see the header on its sums.)"""
     u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
     M, K, dev, px = _rows(x_codes, "x_codes", (u8,))
     N, _, _, pw = _rows(W_codes, "W_codes", (u8,))

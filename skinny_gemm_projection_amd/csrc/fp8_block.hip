@@ -172,37 +172,79 @@ __device__ __forceinline__ uint32_t gathered(const Fp8Product& a, const Segment&
 
 // ---------------------------------------------------------------- team kernel
 
-// S waves share 16 rows of W and up to 16 * MT rows of x; wave s takes the blocks
+// Sums of the S waves of a workgroup (RT * MT blocks of 16 x 16 each, in the LDS at
+// sums + wave * stride), added in order, and the finished outputs: channels n0 .. of
+// `here` rows from row m0 of y on.
+template <int S, int RT, int MT>
+__device__ __forceinline__ void finish_team(const uint4* sums, int stride, int m0, int here, int n0,
+                                            const Fp8Product& a) {
+    for (int e = threadIdx.x; e < RT * MT * kWave; e += S * kWave) {
+        const int f = e >> 6, l = e & 63;
+        const int m = (f % MT) * 16 + (l & 15), n = n0 + (f / MT) * 16 + 4 * (l >> 4);
+        if (m >= here || n >= a.N) continue;
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const f32x4_t p = __builtin_bit_cast(f32x4_t, sums[s * stride + e]);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) y[v] += p[v];
+        }
+        finish4(a, a.N, m0 + m, n, y);
+    }
+}
+
+// Block of K of a slot.  Rows whose pitch is a multiple of 4 KB have the same block in
+// the same memory channels, and workgroups that all start at block 0 queue there
+// together: such rows are started 7 blocks apart and wrap around.  The slots behind the
+// last are empty (past K).
+__device__ __forceinline__ int block_of(int slot, int first, int slots) {
+    const int t = slot + first;
+    return slot >= slots ? slots : t >= slots ? t - slots : t;
+}
+
+// The workgroup's expert (blockIdx.y-th of those that have rows) and its weights; plain:
+// all rows.
+template <int THREADS, bool GROUPED>
+__device__ __forceinline__ Segment team_segment(const Fp8Product& a, int n0, int Kb, const uint8_t*& wq,
+                                                const float*& ws) {
+    wq = a.wq + (int64_t)n0 * a.K;
+    ws = a.ws + (int64_t)(n0 / kBlockK) * Kb;
+    Segment seg{0, 0, a.M};
+    if constexpr (GROUPED) {
+        int unit, first;
+        seg = find_unit<THREADS>(
+            a.offsets, a.E, a.M, [](int n) { return n > 0 ? 1 : 0; },
+            [](int total) { return (int)blockIdx.y < total ? (int)blockIdx.y : -1; }, &unit, &first);
+        wq += (int64_t)seg.e * a.N * a.K;
+        ws += (int64_t)seg.e * ((a.N + kBlockK - 1) / kBlockK) * Kb;
+    }
+    return seg;
+}
+
+// S waves share 16 * RT rows of W and up to 16 * MT rows of x; wave s takes the blocks
 // s, s + S, ... of K through two LDS slots of its own, W and x both, without a barrier
 // until the sums meet.  Slots are refilled without a condition (past the end a load
 // reads zeros and no memory), so each wait covers the older slot alone.  A load
 // instruction covers 8 rows x 128 bytes, whole lines; piece p of row r sits at place
 // p ^ (r % 8).  An expert's segment is walked 16 * MT rows at a time.
-template <int S, int MT, bool GROUPED>
+template <int S, int RT, int MT, bool GROUPED>
 __global__ __launch_bounds__(S* kWave) void fp8_team_kernel(Fp8Product a) {
     constexpr int P = kBlockK / 16, kRows = 8;
-    constexpr int kSlot = 16 * (1 + MT) * P;
-    static_assert(kSlot >= MT * kWave, "a wave's sums reuse its first slot");
+    constexpr int kSlot = 16 * (RT + MT) * P;
+    static_assert(kSlot >= RT * MT * kWave, "a wave's sums reuse its first slot");
     __shared__ uint4 slot0[S][kSlot], slot1[S][kSlot];
     const int lane = threadIdx.x & (kWave - 1), wave = wave_id_in_block();
     const int row = lane & 15, grp = lane >> 4;
     const int K = a.K, N = a.N, Kb = (K + kBlockK - 1) / kBlockK;
-    const int n0 = blockIdx.x * 16;
-    Segment seg{0, 0, a.M};
-    const uint8_t* wq = a.wq;
-    const float* ws = a.ws + (int64_t)(n0 / kBlockK) * Kb;
-    if constexpr (GROUPED) {
-        int unit, first;
-        seg = find_unit<S * kWave>(
-            a.offsets, a.E, a.M, [](int n) { return n > 0 ? 1 : 0; },
-            [](int total) { return (int)blockIdx.y < total ? (int)blockIdx.y : -1; }, &unit, &first);
-        if (seg.count == 0) return;
-        wq += (int64_t)seg.e * N * K;
-        ws += (int64_t)seg.e * ((N + kBlockK - 1) / kBlockK) * Kb;
-    }
-    const rsrc_t rw = make_rsrc(wq + (int64_t)n0 * K, (uint32_t)min(16, N - n0) * (uint32_t)K);
+    const int n0 = blockIdx.x * 16 * RT;
+    const uint8_t* wq;
+    const float* ws;
+    const Segment seg = team_segment<S * kWave, GROUPED>(a, n0, Kb, wq, ws);
+    if (seg.count == 0) return;
+    const rsrc_t rw = make_rsrc(wq, (uint32_t)min(16 * RT, N - n0) * (uint32_t)K);
     const int lrow = lane / P, kpos = ((lane % P) ^ lrow) * 16;
     const int rounds = max(2, (Kb + S - 1) / S + ((Kb + S - 1) / S & 1));  // an even number
+    const int first = K % 4096 == 0 ? (int)(blockIdx.x * 7u % (uint32_t)(rounds * S)) : 0;
 
     for (int m0 = 0; m0 < seg.count; m0 += 16 * MT) {
         const int here = min(16 * MT, seg.count - m0);
@@ -220,40 +262,49 @@ __global__ __launch_bounds__(S* kWave) void fp8_team_kernel(Fp8Product a) {
             const int r = j * 16 + row;
             srow[j] = gather ? gathered(a, seg, m0 + r, 4) : r < here ? (uint32_t)r * 4u : kPastEnd;
         }
-        f32x4_t acc[MT];
+        f32x4_t acc[RT][MT];
 #pragma unroll
-        for (int j = 0; j < MT; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         float f0[MT], f1[MT], w0, w1;
         auto load = [&](int round, uint4* slot, float (&f)[MT], float& wf) {
-            const int b = round * S + wave, k = b * kBlockK + kpos;
+            const int b = block_of(round * S + wave, first, rounds * S), k = b * kBlockK + kpos;
             const uint32_t at = k < K ? (uint32_t)lrow * K + k : kPastEnd;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2 * RT; ++i)
                 load_to_lds<kStream>(rw, slot + i * kWave, at + (uint32_t)(i * kRows * K));
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i)
-                load_to_lds<kCached>(rx, slot + 16 * P + i * kWave,
+                load_to_lds<kCached>(rx, slot + 16 * RT * P + i * kWave,
                                      k < K && xrow[i] != kPastEnd ? xrow[i] + k : kPastEnd);
-            const bool in = b < Kb;
-            const rsrc_t rs = make_rsrc(a.xs + (in ? (int64_t)b * a.x_rows + base : 0),
-                                        in ? (uint32_t)(gather ? a.x_rows : here) * 4u : 0u);
+            const int in = min(b, max(Kb - 1, 0));
+            const rsrc_t rs = make_rsrc(a.xs + (int64_t)in * a.x_rows + base,
+                                        b < Kb ? (uint32_t)(gather ? a.x_rows : here) * 4u : 0u);
 #pragma unroll
             for (int j = 0; j < MT; ++j)
                 f[j] = as_f(__builtin_amdgcn_raw_buffer_load_b32(rs, srow[j], 0, 0));
-            wf = in ? ws[b] : 0.0f;
+            wf = as_f(__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(ws, (uint32_t)Kb * 4u), b * 4, 0, 0));
         };
         auto multiply = [&](const uint4* slot, const float (&f)[MT], float wf) {
-            Frag<true> w;
+            Frag<true> w[RT];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) w.set(t, slot[row * P + ((t * 4 + grp) ^ (row & 7))]);
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    w[i].set(t, slot[(i * 16 + row) * P + ((t * 4 + grp) ^ (row & 7))]);
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 Frag<true> x;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    x.set(t, slot[((1 + j) * 16 + row) * P + ((t * 4 + grp) ^ (row & 7))]);
-                add_scaled(acc[j], block_sum(w, x), f[j] * wf);
-                asm volatile("" : "+v"(acc[j]));  // before the refill, whose loads the factors await
+                    x.set(t, slot[((RT + j) * 16 + row) * P + ((t * 4 + grp) ^ (row & 7))]);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    add_scaled(acc[i][j], block_sum(w[i], x), f[j] * wf);
+                    // before the refill, whose loads the factors await
+                    asm volatile("" : "+v"(acc[i][j]));
+                }
             }
         };
         load(0, slot0[wave], f0, w0);
@@ -268,20 +319,12 @@ __global__ __launch_bounds__(S* kWave) void fp8_team_kernel(Fp8Product a) {
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the end
 #pragma unroll
-        for (int j = 0; j < MT; ++j) slot0[wave][j * kWave + lane] = __builtin_bit_cast(uint4, acc[j]);
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+                slot0[wave][(i * MT + j) * kWave + lane] = __builtin_bit_cast(uint4, acc[i][j]);
         __syncthreads();
-        for (int e = threadIdx.x; e < MT * kWave; e += S * kWave) {
-            const int l = e & 63, m = (e >> 6) * 16 + (l & 15), n = n0 + 4 * (l >> 4);
-            if (m >= here || n >= N) continue;
-            float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const f32x4_t p = __builtin_bit_cast(f32x4_t, slot0[s][e]);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) y[v] += p[v];
-            }
-            finish4(a, N, seg.begin + m0 + m, n, y);
-        }
+        finish_team<S, RT, MT>(slot0[0], kSlot, seg.begin + m0, here, n0, a);
         __syncthreads();  // the sums are read before the slots are filled again
     }
 }
@@ -742,17 +785,21 @@ struct TileCost {
     int bm, bn;
     int per_cu;      // workgroups a compute unit holds
     int group;       // tiles of x an XCD's run goes down before the next tile of W
-    double full;     // ns per code of K of a round that fills every compute unit
-    double single;   // of a round with at most one workgroup a compute unit
+    // ns per code of K of a round that fills every compute unit, and of one with at most
+    // one workgroup a compute unit: by the FP8 instruction, by the bf16 one
+    double full, single, wide_full, wide_single;
 };
-constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.0, 9.9},
-                               {128, 256, 1, 8, 7.2, 6.2},
-                               {128, 128, 1, 8, 4.1, 3.9},
-                               {64, 128, 2, 8, 6.4, 3.6},
-                               {64, 256, 1, 8, 5.0, 4.5}};
+// Fitted to the times of every form at 253 sizes of 24 to 2049 rows, 700 to 36864
+// channels and 1040 to 16384 codes: the form with the least estimate takes 1 % longer
+// than the fastest on average, and more than a tenth at 3 sizes (at most 1.39 times).
+constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.2, 9.3, 0, 0},
+                               {128, 256, 1, 8, 7.5, 7.2, 13.4, 12.0},
+                               {128, 128, 1, 8, 4.3, 4.3, 7.4, 8.0},
+                               {64, 128, 2, 8, 5.9, 3.3, 7.6, 5.5},
+                               {64, 256, 1, 8, 5.6, 4.9, 7.9, 8.1}};
 constexpr int kTileVariants = 5;
 constexpr int kCus = 256;
-constexpr int kTeamMaxM = 64;
+constexpr int kTeamMaxM = 32;
 
 template <class T, int OUT, bool WIDE>
 void launch_tiles(const Fp8Product& a, int S, int kc, int group, float* partial, hipStream_t stream) {
@@ -790,52 +837,85 @@ void launch_grouped_tiles(const Fp8Product& a, hipStream_t stream) {
                        0, 0, 0, a.K, nullptr);
 }
 
-template <bool GROUPED>
-void launch_team(int mt, const Fp8Product& a, hipStream_t stream) {
-    constexpr int S = 8;
-    const dim3 grid((uint32_t)ceil_div(a.N, 16), GROUPED ? (a.E < a.M ? a.E : a.M) : 1), block(S * kWave);
-    if (mt == 1) {
-        hipLaunchKernelGGL((fp8_team_kernel<S, 1, GROUPED>), grid, block, 0, stream, a);
-    } else if (mt == 2 || GROUPED) {
-        hipLaunchKernelGGL((fp8_team_kernel<S, 2, GROUPED>), grid, block, 0, stream, a);
-    } else if constexpr (!GROUPED) {
-        if (mt == 3)
-            hipLaunchKernelGGL((fp8_team_kernel<S, 3, GROUPED>), grid, block, 0, stream, a);
-        else
-            hipLaunchKernelGGL((fp8_team_kernel<S, 4, GROUPED>), grid, block, 0, stream, a);
+template <int S, int RT, int MT, bool GROUPED>
+void launch_team(const Fp8Product& a, hipStream_t stream) {
+    hipLaunchKernelGGL((fp8_team_kernel<S, RT, MT, GROUPED>),
+                       dim3((uint32_t)ceil_div(a.N, 16 * RT), GROUPED ? (a.E < a.M ? a.E : a.M) : 1),
+                       dim3(S * kWave), 0, stream, a);
+}
+
+// The forms that the plans below name.
+void launch_few_rows(const Fp8BlockPlan& p, const Fp8Product& a, hipStream_t stream) {
+    if (a.offsets) return launch_team<2, 2, 1, true>(a, stream);
+    if (p.mt == 1) {
+        if (p.rt == 1) return launch_team<8, 1, 1, false>(a, stream);
+        if (p.waves == 8) return launch_team<8, 2, 1, false>(a, stream);
+        return launch_team<4, 2, 1, false>(a, stream);
     }
+    if (p.rt == 1) return launch_team<8, 1, 2, false>(a, stream);
+    if (p.waves == 8) return launch_team<8, 2, 2, false>(a, stream);
+    return launch_team<4, 2, 2, false>(a, stream);
 }
 
 }  // namespace
 
+// Up to 32 rows a team's form by the workgroups that 16 channels each would make.
+// Measured (us, weights from HBM; waves, 16-row tiles of W a workgroup):
+//                        8, 1   8, 2   4, 1   4, 2
+//    16 x  1024 x 7168    7.6   10.0    9.3   12.0
+//    16 x  4096 x 7168    8.8   10.9   10.3   12.8
+//    16 x  7168 x 8192   14.9   12.8   14.2   14.9
+//    16 x  8192 x 7168   14.6   12.7   13.4   14.3
+//    16 x 36864 x 7168   54     54.2   53.0   47.1
+//    32 x  4096 x 7168   11.6   13.8   13.3
+//    32 x  8192 x 7168   20.1   15.5   17.5   16.7
+//    32 x 36864 x 7168   87     66            58.2
+// (From 33 rows tiles: 48 x 8192 x 7168 17.7 in tiles of 64 x 128 split four ways, 19.0
+// by the best team.)
+// Tiles: 5 us, then rounds of workgroups at the fitted cost per code, but no faster than
+// W comes; a split adds the reduction's launch and its traffic.
 Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide) {
-    if (M <= kTeamMaxM) return Fp8BlockPlan{Fp8BlockPlan::kTeam, (M + 15) / 16, 0, 1, K, 0, true};
+    if (M <= kTeamMaxM) {
+        const int64_t wgs = ceil_div(N, 16);
+        const int rt = wgs <= kCus ? 1 : 2, waves = wgs <= 2 * kCus ? 8 : 4;
+        return Fp8BlockPlan{Fp8BlockPlan::kTeam, M <= 16 ? 1 : 2, rt, waves, 0, 1, K, 0, true};
+    }
+    const double stream = (double)N * K / (wide ? 4.1e6 : 9.1e6);
     Fp8BlockPlan best{};
     double least = 1e30;
     for (int v = wide ? 1 : 0; v < kTileVariants; ++v) {
         const TileCost& c = kTiles[v];
+        const double full = wide ? c.wide_full : c.full, single = wide ? c.wide_single : c.single;
         const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn);
         for (int S = 1; S <= 16; ++S) {
             const int kc = S == 1 ? K : (int)ceil_div(ceil_div(K, S), kBlockK) * kBlockK;
             if (S > 1 && (kc < 4 * kBlockK || (int64_t)(S - 1) * kc >= K)) break;
             const int64_t wgs = tiles * S, slots = (int64_t)kCus * c.per_cu, rem = wgs % slots;
-            double est = 3.0 + kc * (wgs / slots * c.full + (rem == 0 ? 0.0 : rem <= kCus ? c.single : c.full)) / 1000.0;
+            const double rounds = wgs / slots * full + (rem == 0 ? 0.0 : rem <= kCus ? single : full);
+            double est = ceil_div(kc, kBlockK) * kBlockK * rounds / 1000.0;
+            est = 5.0 + (est > stream ? est : stream);
             const size_t ws = S > 1 ? (size_t)S * tiles * c.bm * c.bn * 4 : 0;
-            if (S > 1) est += 3.0 + 8.0 * S * M * N / 4.0e6;
+            if (S > 1) est += 1.9 + 7.2 * S * M * N / 4.0e6;
             if (est < least && ws <= ((size_t)1 << 30)) {
                 least = est;
-                best = Fp8BlockPlan{Fp8BlockPlan::kTile, 0, v, S, kc, ws, wide};
+                best = Fp8BlockPlan{Fp8BlockPlan::kTile, 0, 0, 0, v, S, kc, ws, wide};
             }
         }
     }
     return best;
 }
 
+// Few rows an expert: teams of 2 waves, 6 workgroups a compute unit, so that one's look
+// for its expert is hidden behind the others' streams (experts of 4 tokens, 1 GB: 174 us
+// the step against 266 with 8 waves, 180 with 4).  From 6 rows on average tiles of 64
+// rows, which also bound what one popular expert costs (48 experts, 64 tokens of 8: 374
+// us against 431; 32 tokens 361 against 334).
 Fp8BlockPlan fp8_grouped_plan(int M, int E, int N, int K, bool wide) {
+    (void)N;
     const int64_t rows = M / (E < M ? E : M);  // an expert's, on average
-    if (rows <= 24) return Fp8BlockPlan{Fp8BlockPlan::kTeam, rows <= 4 ? 1 : 2, 0, 1, K, 0, true};
+    if (rows <= 5) return Fp8BlockPlan{Fp8BlockPlan::kTeam, 1, 2, 2, 0, 1, K, 0, true};
     const int tile = rows <= 64 ? 4 : rows <= 160 || wide ? 1 : 0;
-    return Fp8BlockPlan{Fp8BlockPlan::kTile, 0, tile, 1, K, 0, wide};
+    return Fp8BlockPlan{Fp8BlockPlan::kTile, 0, 0, 0, tile, 1, K, 0, wide};
 }
 
 bool fp8_gated_ok(const Fp8BlockPlan& p, int F) {
@@ -860,10 +940,7 @@ hipError_t launch_fp8_block(const Fp8BlockPlan& p, const Fp8Product& product, vo
     Fp8Product a = product;
     a.ld = a.N;
     if (p.kind == Fp8BlockPlan::kTeam) {
-        if (a.offsets)
-            launch_team<true>(p.mt, a, stream);
-        else
-            launch_team<false>(p.mt, a, stream);
+        launch_few_rows(p, a, stream);
         return hipGetLastError();
     }
     with_tile(p.tile, [&](auto shape) {

@@ -254,7 +254,7 @@ struct Fp8Product {
 // What runs for a size.
 struct Fp8BlockPlan {
     enum Kind { kTeam, kTile } kind;
-    int mt;                // team kernel: 16-row tiles of x
+    int mt, rt, waves;     // team kernel: 16-row tiles of x and of W, waves a workgroup
     int tile, S, kc;       // tile kernel: variant, K splits, codes a split
     size_t workspace;      // bytes of fp32 partial sums (S > 1)
     bool wide;             // the bf16 instruction: sums at fp32's precision
