@@ -66,15 +66,26 @@ struct Frag {
     }
 };
 
+__device__ __forceinline__ Frag<true> widened(const Frag<false>& codes) {
+    Frag<true> f;
+    f.set(0, codes.v[0]);
+    f.set(1, codes.v[1]);
+    return f;
+}
+
+// Products of a quarter of the block, added to s.
+__device__ __forceinline__ f32x4_t quarter_sum(const Frag<true>& w, const Frag<true>& x, int q, f32x4_t s) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w.v[q]),
+                                                   __builtin_bit_cast(bf16x8_t, x.v[q]), s, 0, 0, 0);
+}
+
 // The block's sum of products.
 template <bool WIDE>
 __device__ __forceinline__ f32x4_t block_sum(const Frag<WIDE>& w, const Frag<WIDE>& x) {
     f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (WIDE) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w.v[i]),
-                                                        __builtin_bit_cast(bf16x8_t, x.v[i]), s, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) s = quarter_sum(w, x, i, s);
     } else {
         struct Two {
             uint4 a, b;
@@ -501,12 +512,18 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
     };
     const std::integral_constant<int, 0> c0;
     const std::integral_constant<int, 1> c1;
+    // Load l of a stage: W, the scales, then the first part of x.
+    auto load_any = [&](auto i, int k0, auto lc) {
+        constexpr int l = decltype(lc)::value;
+        if constexpr (l < T::LW)
+            load_w(i, k0, l);
+        else if constexpr (l == T::LW)
+            load_scales(i, k0);
+        else
+            load_x(i, c0, k0, l - T::LW - 1);
+    };
     auto load_stage = [&](auto i, int k0) {
-#pragma unroll
-        for (int l = 0; l < T::LW; ++l) load_w(i, k0, l);
-        load_scales(i, k0);
-#pragma unroll
-        for (int l = 0; l < kHalf; ++l) load_x(i, c0, k0, l);
+        unrolled<0, T::LW + 1 + kHalf>([&](auto lc) { load_any(i, k0, lc); });
     };
 
     f32x4_t acc[FN][FM];
@@ -519,7 +536,9 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
     const int xat = (T::tile_row(wm, 0) + row) * P, wat = (wn * FN * 16 + row) * P;
     const int piece0 = grp ^ (row & 7), piece1 = (4 + grp) ^ (row & 7);
     const int n = max(1, (kend - kbeg + kBlockK - 1) / kBlockK);
-    Frag<WIDE> fw[FN], fx[2];
+    Frag<WIDE> fw[FN];
+    Frag<false> fx[2];
+    Frag<true> wide_x[2];
     auto read_w = [&](auto i, int c) {
         const uint4* b = w_buffer(i);
         fw[c].set(0, b[wat + c * 16 * P + piece0]);
@@ -541,13 +560,14 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
 #pragma unroll
     for (int c = 0; c < FN; ++c) part[1][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     // Loads return in order, and a wait leaves the last kOut out.
+    // A stage's loads are spread over its tiles of x: waves that issue all of theirs at once
+    // hold each other, and their products, up for as long as the products take (1024 x 8192
+    // x 7168 66 -> 60 us, with fp32 outputs 109 -> 99).
     // Three or four buffers: stage s begins when its loads have landed for every wave
     // (those of the stages s + 1 .. s + NB - 2 may be out); then the buffer of stage s - 1,
     // all of whose reads are done, is refilled with stage s + NB - 1.
-    // Two buffers: a stage's loads are spread over its tiles of x, since waves that issue
-    // all of theirs at once hold each other (and their products) up for as long as the
-    // products take.  So that the late ones still have more than a stage to land, parts of
-    // a buffer are refilled as soon as all waves have read them:
+    // Two buffers: so that the late loads still have more than a stage to land, parts of a
+    // buffer are refilled as soon as all waves have read them:
     //  * from the first tile on, the second half of x of stage s + 1;
     //  * from the middle, when every wave holds W and the scales in registers and has read
     //    the first half of x, those of stage s + 2 (there the second half of stage s has to
@@ -566,10 +586,7 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
         auto stage = [&](auto i, int s) {  // s % NB == i
             const std::integral_constant<int, (decltype(i)::value + NB - 1) % NB> next;
             const int k_next = (s + NB - 1) * kBlockK;
-            if constexpr (!T::kParts) {
-                wait_and_barrier<kOut>();
-                load_stage(next, k_next);
-            }
+            if constexpr (!T::kParts) wait_and_barrier<kOut>();
             const float* sx = scales(i);
             float ws[kScales], xs[ACT];
 #pragma unroll
@@ -580,6 +597,10 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
 #pragma unroll
                 for (int c = 0; c < FN; ++c) read_w(i, c);
                 read_x(i, c0);
+                if constexpr (WIDE) {
+                    read_x(i, c1);
+                    wide_x[0] = widened(fx[0]);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
             unrolled<0, ACT>([&](auto jc) {
@@ -593,40 +614,53 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
                         // W, the scales and the first half of x over the tiles left but the last
                         constexpr int kAll = T::LW + 1 + kHalf, kOver = kSecond ? ACT - 1 - kMiddle : 1;
                         constexpr int kAt = j - kMiddle;
-                        unrolled<kAll * kAt / kOver, kAll*(kAt + 1) / kOver>([&](auto lc) {
-                            constexpr int l = decltype(lc)::value;
-                            if constexpr (l < T::LW)
-                                load_w(i, k2, l);
-                            else if constexpr (l == T::LW)
-                                load_scales(i, k2);
-                            else
-                                load_x(i, c0, k2, l - T::LW - 1);
-                        });
+                        unrolled<kAll * kAt / kOver, kAll*(kAt + 1) / kOver>([&](auto lc) { load_any(i, k2, lc); });
                     }
                     __builtin_amdgcn_sched_barrier(0);
+                } else {
+                    constexpr int kAll = T::LW + 1 + T::LX;
+                    unrolled<kAll * j / ACT, kAll*(j + 1) / ACT>([&](auto lc) { load_any(next, k_next, lc); });
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                if constexpr (j + 1 < ACT)
-                    read_x(i, std::integral_constant<int, j + 1>{});
+                constexpr int kNext = j + (WIDE ? 2 : 1);
+                if constexpr (kNext < ACT)
+                    read_x(i, std::integral_constant<int, kNext>{});
                 else if constexpr (kLast)
                     read_x(next, c0);
                 // ahead of the other wave of the SIMD while it loads: 403 -> 396 us at 8192 x 8192 x 7168
                 __builtin_amdgcn_s_setprio(1);
+                if constexpr (WIDE) {
+                    // the next tile's codes are widened between the products of this one
+#pragma unroll
+                    for (int c = 0; c < FN; ++c) part[j % 2][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int c = 0; c < FN; ++c)
+                            part[j % 2][c] = quarter_sum(fw[c], wide_x[j % 2], q, part[j % 2][c]);
+                    if constexpr (j + 1 < ACT) wide_x[(j + 1) % 2] = widened(fx[(j + 1) % 2]);
+                }
 #pragma unroll
                 for (int c = 0; c < FN; ++c) {
-                    part[j % 2][c] = block_sum(fw[c], fx[j % 2]);
-                    if constexpr (kLast) read_w(next, c);
+                    if constexpr (!WIDE) {
+                        part[j % 2][c] = block_sum(fw[c], fx[j % 2]);
+                        if constexpr (kLast) read_w(next, c);
+                    }
                     add_scaled(acc[c][prev], part[(j + 1) % 2][c], f[(j + 1) % 2][c % kScales]);
                     asm volatile("" : "+v"(acc[c][prev]));  // added here, not behind the stage
                 }
 #pragma unroll
                 for (int c = 0; c < kScales; ++c) f[j % 2][c] = xs[j] * ws[c];
-                if constexpr (j + 1 < ACT || kLast) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
-#pragma unroll
-                for (int c = 0; c < FN; ++c) {
-                    __builtin_amdgcn_sched_group_barrier(0x8, WIDE ? 4 : 1, 0);  // matrix instructions
+                if constexpr (kNext < ACT || kLast) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+                constexpr int kProducts = WIDE ? 4 * FN : FN;
+                constexpr int kOthers = 4 * FN + (WIDE && j + 1 < ACT ? 16 : 0);
+                unrolled<0, kProducts>([&](auto gc) {
+                    constexpr int g = decltype(gc)::value;
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);  // matrix instruction
                     if constexpr (kLast) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);  // vector arithmetic
-                }
+                    __builtin_amdgcn_sched_group_barrier(
+                        0x2, kOthers * (g + 1) / kProducts - kOthers * g / kProducts, 0);  // vector arithmetic
+                });
                 __builtin_amdgcn_s_setprio(0);
                 __builtin_amdgcn_sched_barrier(0);  // reads stay one tile ahead: more would not fit
             });
