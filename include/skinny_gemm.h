@@ -85,7 +85,7 @@ typedef enum {
     SG_KERNEL_QUANT_INT8 = 13,  /* per-row int8 codes (optionally of a gated product) */
     SG_KERNEL_FP8_BLOCK = 14,   /* product of block-scaled e4m3 codes, plain or by expert */
     SG_KERNEL_QUANT_FP8 = 15,   /* e4m3 codes and block scales of rows             */
-    SG_KERNEL_MOE_SORT = 16,    /* pairs sorted by expert (one or three launches)  */
+    SG_KERNEL_MOE_SORT = 16,    /* pairs sorted by expert (one to three launches)  */
     SG_KERNEL_MOE_ROWS = 17     /* rows to their experts and back, and gradients   */
 } sg_kernel;
 

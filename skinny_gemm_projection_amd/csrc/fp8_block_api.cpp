@@ -53,7 +53,7 @@ sg_status sort(int32_t T, int32_t topk, int32_t E, const int32_t* ids, int32_t* 
     (void)hipGetLastError();
     const int32_t P = T * topk;
     return done(sg::launch_moe_sort(ids, P, E, offsets, sorted, positions, ws, stream),
-                SG_KERNEL_MOE_SORT, sg::moe_sort_launches(P), "moe_sort", T, topk, E);
+                SG_KERNEL_MOE_SORT, sg::moe_sort_launches(P, E), "moe_sort", T, topk, E);
 }
 
 sg_status product(const sg::Fp8BlockPlan& plan, const sg::Fp8Product& a, void* ws,

@@ -217,7 +217,7 @@ hipError_t launch_quant_fp8(int M, int K, const void* x, bool f32, bool gated, u
 // Pairs sorted by expert and rows brought there and back (moe_rows.hip); pitch: bytes
 // of a row, a multiple of 16 below 2^32.  T * topk <= 2^22, E <= 4096.
 size_t moe_sort_workspace_bytes(int64_t P, int E);
-int moe_sort_launches(int64_t P);
+int moe_sort_launches(int64_t P, int E);
 hipError_t launch_moe_sort(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* sorted,
                            int32_t* positions, void* ws, hipStream_t stream);
 hipError_t launch_moe_gather(const void* x, int T, int topk, int64_t pitch, const int32_t* positions,

@@ -18,6 +18,8 @@
 // A pair has one row and a row one pair, so no two threads write one place.  All
 // row kernels go token by token: the token's own row is read (or written) once, and
 // its topk rows elsewhere once each.
+#include <algorithm>
+
 #include "int8_device.h"
 #include "launch.h"
 
@@ -67,16 +69,25 @@ __device__ __forceinline__ int exclusive_scan(int32_t* s, int n) {
     return total;
 }
 
-// Places of `count` pairs from pair p0 on: cursor[e] holds the next place of
-// expert e.  Waves take 64 pairs each in turn, one wave at a time; inside a wave
-// the lanes of one expert are found by a ballot for each bit of the id.
-template <int THREADS>
+// counts[e] of the pairs [p0, p0 + count), which the given threads of one or more waves
+// take in turn.  (A count: the order of the additions is free.)
+__device__ __forceinline__ void count_pairs(const int32_t* __restrict__ ids, int64_t p0, int count,
+                                            int E, int32_t* counts, int thread, int threads) {
+    for (int c = thread; c < count; c += threads) {
+        const int e = ids[p0 + c];
+        if (e >= 0 && e < E) atomicAdd(&counts[e], 1);
+    }
+}
+
+// Places of the pairs [p0, p0 + count) by one wave, 64 at a time: cursor[e] holds the next
+// place of expert e, and the lanes of one expert are found by a ballot for each bit of
+// the id.  LDS serves a wave in order, so every lane reads a cursor before it moves.
 __device__ __forceinline__ void place_pairs(const int32_t* __restrict__ ids, int64_t p0, int count,
                                             int E, int bits, int32_t* cursor, int32_t* sorted,
                                             int32_t* positions) {
-    const int lane = threadIdx.x & (kWave - 1), wave = wave_id_in_block();
-    for (int c0 = 0; c0 < count; c0 += THREADS) {
-        const int c = c0 + threadIdx.x;
+    const int lane = threadIdx.x & (kWave - 1);
+    for (int c0 = 0; c0 < count; c0 += kWave) {
+        const int c = c0 + lane;
         const int e = c < count ? ids[p0 + c] : -1;
         const bool ok = e >= 0 && e < E;
         uint64_t same = __ballot(ok);
@@ -85,16 +96,9 @@ __device__ __forceinline__ void place_pairs(const int32_t* __restrict__ ids, int
             same &= (e >> b) & 1 ? set : ~set;
         }
         const int rank = __popcll(same & ((1ull << lane) - 1));
-        int at = 0;
-        const int turns = min(THREADS, count - c0);
-        for (int w = 0; w * kWave < turns; ++w) {  // the same number of turns for every wave
-            if (w == wave && ok) {
-                at = cursor[e];
-                // the reads of all lanes are before this write: one wave, in order
-                if (rank == 0) cursor[e] = at + __popcll(same);
-            }
-            __syncthreads();
-        }
+        volatile int32_t* next = cursor;
+        const int at = ok ? next[e] : 0;
+        if (ok && rank == 0) next[e] = at + __popcll(same);
         if (c < count) {
             positions[p0 + c] = ok ? at + rank : -1;
             if (ok && sorted) sorted[at + rank] = (int32_t)(p0 + c);
@@ -102,41 +106,85 @@ __device__ __forceinline__ void place_pairs(const int32_t* __restrict__ ids, int
     }
 }
 
-__device__ __forceinline__ void count_pairs(const int32_t* __restrict__ ids, int64_t p0, int count,
-                                            int E, int32_t* counts, int threads) {
-    for (int e = threadIdx.x; e < E; e += threads) counts[e] = 0;
-    __syncthreads();
-    for (int c = threadIdx.x; c < count; c += threads) {
-        const int e = ids[p0 + c];
-        if (e >= 0 && e < E) atomicAdd(&counts[e], 1);  // a count: the order is free
+constexpr int kSortMaxExperts = 4096;
+constexpr int kSortOneMax = 4096;      // pairs one workgroup sorts alone
+constexpr int kSortChunk = 1024;       // pairs of a workgroup beyond, in two launches,
+constexpr int kSortTwoMax = 1 << 16;   // up to so many pairs
+constexpr int64_t kSortTwoWork = 1 << 27;  // and pairs * experts;
+constexpr int kSortBigChunk = 4096;    // past them three launches
+
+// The sort of one workgroup's pairs [p0, p0 + count): every wave counts its share of them,
+// the shares' counts become first places, and every wave places its own.  before(e): the
+// pairs of expert e in front of p0; base[e] comes in as the pairs of all experts below e.
+// s: LDS for the waves' counts, [WAVES][E].
+template <int WAVES, class Before>
+__device__ __forceinline__ void sort_share(const int32_t* __restrict__ ids, int64_t p0, int count, int E,
+                                           int bits, int32_t* s, const int32_t* base, Before before,
+                                           int32_t* sorted, int32_t* positions) {
+    const int wave = wave_id_in_block();
+    const int share = (count + WAVES * kWave - 1) / (WAVES * kWave) * kWave;
+    const int lo = min(count, wave * share), n = min(share, count - lo);
+    for (int e = threadIdx.x; e < E; e += WAVES * kWave) {
+        int run = base[e] + before(e);
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const int c = s[w * E + e];
+            s[w * E + e] = run;
+            run += c;
+        }
     }
     __syncthreads();
+    place_pairs(ids, p0 + lo, n, E, bits, s + wave * E, sorted, positions);
 }
 
-constexpr int kSortOneMax = 4096;   // pairs one workgroup sorts alone
-constexpr int kSortChunk = 2048;    // pairs of a workgroup beyond
-constexpr int kSortMaxExperts = 4096;
+// Every wave's counts of its share, and the sum of all in total[e].
+template <int WAVES>
+__device__ __forceinline__ void count_shares(const int32_t* __restrict__ ids, int64_t p0, int count,
+                                             int E, int32_t* s, int32_t* total) {
+    const int wave = wave_id_in_block(), lane = threadIdx.x & (kWave - 1);
+    const int share = (count + WAVES * kWave - 1) / (WAVES * kWave) * kWave;
+    const int lo = min(count, wave * share), n = min(share, count - lo);
+    for (int e = threadIdx.x; e < WAVES * E; e += WAVES * kWave) s[e] = 0;
+    __syncthreads();
+    count_pairs(ids, p0 + lo, n, E, s + wave * E, lane, kWave);
+    __syncthreads();
+    if (total) {
+        for (int e = threadIdx.x; e < E; e += WAVES * kWave) {
+            int sum = 0;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) sum += s[w * E + e];
+            total[e] = sum;
+        }
+        __syncthreads();
+    }
+}
 
-__global__ __launch_bounds__(1024) void moe_sort_one_kernel(const int32_t* __restrict__ ids, int P,
-                                                            int E, int bits, int32_t* offsets,
-                                                            int32_t* sorted, int32_t* positions) {
-    __shared__ int32_t cursor[kSortMaxExperts];
-    count_pairs(ids, 0, P, E, cursor, 1024);
-    const int total = exclusive_scan<1024>(cursor, E);
-    for (int e = threadIdx.x; e < E; e += 1024) offsets[e] = cursor[e];
+// LDS: counts of WAVES waves and their sums, (WAVES + 1) * E.
+template <int WAVES>
+__global__ __launch_bounds__(WAVES* kWave) void moe_sort_one_kernel(const int32_t* __restrict__ ids,
+                                                                    int P, int E, int bits,
+                                                                    int32_t* offsets, int32_t* sorted,
+                                                                    int32_t* positions) {
+    extern __shared__ int32_t lds[];
+    int32_t* base = lds + WAVES * E;
+    count_shares<WAVES>(ids, 0, P, E, lds, base);
+    const int total = exclusive_scan<WAVES * kWave>(base, E);
+    for (int e = threadIdx.x; e < E; e += WAVES * kWave) offsets[e] = base[e];
     if (threadIdx.x == 0) offsets[E] = total;
-    __syncthreads();  // the offsets are read before the cursors move
-    place_pairs<1024>(ids, 0, P, E, bits, cursor, sorted, positions);
+    sort_share<WAVES>(ids, 0, P, E, bits, lds, base, [](int) { return 0; }, sorted, positions);
     if (sorted)
-        for (int i = total + threadIdx.x; i < P; i += 1024) sorted[i] = -1;
+        for (int i = total + threadIdx.x; i < P; i += WAVES * kWave) sorted[i] = -1;
 }
 
 // counts[chunk][e] of the pairs of a chunk
 __global__ __launch_bounds__(kBlock) void moe_count_kernel(const int32_t* __restrict__ ids, int P,
-                                                           int E, int32_t* counts) {
+                                                           int chunk, int E, int32_t* counts) {
     __shared__ int32_t s[kSortMaxExperts];
-    const int64_t p0 = (int64_t)blockIdx.x * kSortChunk;
-    count_pairs(ids, p0, (int)min((int64_t)kSortChunk, P - p0), E, s, kBlock);
+    const int64_t p0 = (int64_t)blockIdx.x * chunk;
+    for (int e = threadIdx.x; e < E; e += kBlock) s[e] = 0;
+    __syncthreads();
+    count_pairs(ids, p0, (int)min((int64_t)chunk, P - p0), E, s, threadIdx.x, kBlock);
+    __syncthreads();
     for (int e = threadIdx.x; e < E; e += kBlock) counts[(int64_t)blockIdx.x * E + e] = s[e];
 }
 
@@ -165,25 +213,46 @@ __global__ __launch_bounds__(kWave) void moe_scan_kernel(int32_t* counts, int ch
     totals[e] = run;
 }
 
+// The chunks' places.  SUMMED: counts are sums over the chunks before, with totals;
+// otherwise each workgroup adds the few chunks' counts itself, which saves a launch.
+// LDS: counts of the waves, the experts' first places and the pairs before, (waves + 2) * E.
+template <bool SUMMED>
 __global__ __launch_bounds__(kBlock) void moe_place_kernel(const int32_t* __restrict__ ids, int P,
-                                                           int E, int bits,
-                                                           const int32_t* __restrict__ before,
+                                                           int chunk, int chunks, int E, int bits,
+                                                           const int32_t* __restrict__ counts,
                                                            const int32_t* __restrict__ totals,
                                                            int32_t* offsets, int32_t* sorted,
                                                            int32_t* positions) {
-    __shared__ int32_t cursor[kSortMaxExperts];
-    for (int e = threadIdx.x; e < E; e += kBlock) cursor[e] = totals[e];
-    __syncthreads();
-    const int total = exclusive_scan<kBlock>(cursor, E);
+    extern __shared__ int32_t lds[];
+    int32_t* base = lds + kWavesPerBlock * E;
+    int32_t* before = base + E;
+    const int b = blockIdx.x;
     for (int e = threadIdx.x; e < E; e += kBlock) {
-        if (blockIdx.x == 0) offsets[e] = cursor[e];
-        cursor[e] += before[(int64_t)blockIdx.x * E + e];
+        if constexpr (SUMMED) {
+            base[e] = totals[e];
+            before[e] = counts[(int64_t)b * E + e];
+        } else {
+            int all = 0, front = 0;
+#pragma unroll 8
+            for (int c = 0; c < chunks; ++c) {
+                const int v = counts[(int64_t)c * E + e];
+                all += v;
+                front += c < b ? v : 0;
+            }
+            base[e] = all;
+            before[e] = front;
+        }
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = total;
-    __syncthreads();
-    const int64_t p0 = (int64_t)blockIdx.x * kSortChunk;
-    const int count = (int)min((int64_t)kSortChunk, P - p0);
-    place_pairs<kBlock>(ids, p0, count, E, bits, cursor, sorted, positions);
+    const int64_t p0 = (int64_t)b * chunk;
+    const int count = (int)min((int64_t)chunk, P - p0);
+    count_shares<kWavesPerBlock>(ids, p0, count, E, lds, nullptr);
+    const int total = exclusive_scan<kBlock>(base, E);
+    if (b == 0) {
+        for (int e = threadIdx.x; e < E; e += kBlock) offsets[e] = base[e];
+        if (threadIdx.x == 0) offsets[E] = total;
+    }
+    sort_share<kWavesPerBlock>(ids, p0, count, E, bits, lds, base, [&](int e) { return before[e]; }, sorted,
+                               positions);
     if (sorted)  // behind the last valid pair
         for (int i = threadIdx.x; i < count; i += kBlock)
             if (p0 + i >= total) sorted[p0 + i] = -1;
@@ -353,10 +422,31 @@ dim3 token_grid(int T, int64_t pitch) {
 
 }  // namespace
 
+// One workgroup takes 8.2 us for 4096 pairs of 384 experts and 12.6 for 8192, two
+// launches 10.8 and 9.9.  In two launches every workgroup adds the counts of all chunks
+// itself: 12.3 us for 32768 pairs of 384 experts (three launches: 25.6) and 22.3 for 65536
+// of 1024 (28.2), but 55.5 for 65536 of 4096 (38.3; for half of them 36.8 and 38.1).
+int moe_sort_launches(int64_t P, int E) {
+    return P <= kSortOneMax ? 1 : P <= kSortTwoMax && P * E <= kSortTwoWork ? 2 : 3;
+}
+
+// Never less for more pairs, so a workspace for the most of them serves all.
 size_t moe_sort_workspace_bytes(int64_t P, int E) {
     if (P <= kSortOneMax) return 0;
-    const int64_t chunks = (P + kSortChunk - 1) / kSortChunk;
-    return (size_t)(chunks + 1) * E * 4;
+    const int64_t small = (std::min<int64_t>(P, kSortTwoMax) + kSortChunk - 1) / kSortChunk;
+    const int64_t big = (P + kSortBigChunk - 1) / kSortBigChunk;
+    return (size_t)(std::max(small, big) + 1) * E * 4;
+}
+
+// One of the sorting kernels, each with `ints` ints of LDS.
+template <class... P, class... A>
+static hipError_t launch_sort(void (*kernel)(P...), int grid, int block, size_t ints, hipStream_t stream,
+                              A... args) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)(ints * 4));
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), ints * 4, stream, args...);
+    return hipGetLastError();
 }
 
 hipError_t launch_moe_sort(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* sorted,
@@ -364,22 +454,30 @@ hipError_t launch_moe_sort(const int32_t* ids, int P, int E, int32_t* offsets, i
     int bits = 0;
     while ((1 << bits) < E) ++bits;
     if (P <= kSortOneMax) {
-        hipLaunchKernelGGL(moe_sort_one_kernel, dim3(1), dim3(1024), 0, stream, ids, P, E, bits,
+        // 16 waves while their counts take at most 68 KB of LDS, and are needed
+        if (E <= 1024 && P > 4 * kWave)
+            return launch_sort(moe_sort_one_kernel<16>, 1, 16 * kWave, (size_t)17 * E, stream, ids, P, E,
+                               bits, offsets, sorted, positions);
+        return launch_sort(moe_sort_one_kernel<4>, 1, 4 * kWave, (size_t)5 * E, stream, ids, P, E, bits,
                            offsets, sorted, positions);
-        return hipGetLastError();
     }
-    const int chunks = (P + kSortChunk - 1) / kSortChunk;
+    const bool two = moe_sort_launches(P, E) == 2;
+    const int chunk = two ? kSortChunk : kSortBigChunk, chunks = (P + chunk - 1) / chunk;
+    const size_t ints = (size_t)(kWavesPerBlock + 2) * E;
     int32_t* counts = static_cast<int32_t*>(ws);
     int32_t* totals = counts + (int64_t)chunks * E;
-    hipLaunchKernelGGL(moe_count_kernel, dim3(chunks), dim3(kBlock), 0, stream, ids, P, E, counts);
+    hipLaunchKernelGGL(moe_count_kernel, dim3(chunks), dim3(kBlock), 0, stream, ids, P, chunk, E, counts);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (two)
+        return launch_sort(moe_place_kernel<false>, chunks, kBlock, ints, stream, ids, P, chunk, chunks, E,
+                           bits, counts, totals, offsets, sorted, positions);
     hipLaunchKernelGGL(moe_scan_kernel, dim3((E + kWave - 1) / kWave), dim3(kWave), 0, stream, counts,
                        chunks, E, totals);
-    hipLaunchKernelGGL(moe_place_kernel, dim3(chunks), dim3(kBlock), 0, stream, ids, P, E, bits,
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    return launch_sort(moe_place_kernel<true>, chunks, kBlock, ints, stream, ids, P, chunk, chunks, E, bits,
                        counts, totals, offsets, sorted, positions);
-    return hipGetLastError();
 }
-
-int moe_sort_launches(int64_t P) { return P <= kSortOneMax ? 1 : 3; }
 
 hipError_t launch_moe_gather(const void* x, int T, int topk, int64_t pitch, const int32_t* positions,
                              void* rows, hipStream_t stream) {

@@ -14,7 +14,8 @@ BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
 
 SORT = [(0, 3, 5), (1, 1, 1), (1, 8, 384), (3, 32, 4096), (64, 1, 2), (65, 8, 7), (512, 8, 384),
         (4096, 1, 1), (4097, 1, 3), (513, 8, 130), (1025, 4, 4096), (5000, 8, 384), (2048, 2, 64),
-        (100, 32, 50), (20011, 6, 48)]
+        (100, 32, 50), (20011, 6, 48), (37, 7, 1025), (64, 4, 1024), (8191, 8, 4096), (8193, 8, 384),
+        (32768, 2, 3)]
 
 
 @pytest.mark.parametrize("T,topk,E", SORT)
@@ -33,7 +34,9 @@ def test_sort(T, topk, E, kind):
     before = sg.skinny_gemm_get_counters()
     got = sg.skinny_moe_sort(ids.to(DEV), E)
     ran = counters_delta(before, sg.skinny_gemm_get_counters())
-    assert ran[sg.SG_KERNEL_MOE_SORT] == sum(ran) == (1 if T * topk <= 4096 else 3)
+    P = T * topk
+    assert ran[sg.SG_KERNEL_MOE_SORT] == sum(ran) == (
+        1 if P <= 4096 else 2 if P <= 1 << 16 and P * E <= 1 << 27 else 3)
     for a, b, name in zip(got, (offsets, order, positions), ("offsets", "sorted", "positions")):
         assert torch.equal(a.cpu(), b), name
 
