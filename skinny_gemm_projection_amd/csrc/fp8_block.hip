@@ -823,14 +823,14 @@ struct TileCost {
     // one workgroup a compute unit: by the FP8 instruction, by the bf16 one
     double full, single, wide_full, wide_single;
 };
-// Fitted to the times of every form at 253 sizes of 24 to 2049 rows, 700 to 36864
+// Fitted to the times of every form at 198 sizes of 40 to 2049 rows, 700 to 36864
 // channels and 1040 to 16384 codes: the form with the least estimate takes 1 % longer
-// than the fastest on average, and more than a tenth at 3 sizes (at most 1.39 times).
-constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.2, 9.3, 0, 0},
-                               {128, 256, 1, 8, 7.5, 7.2, 13.4, 12.0},
-                               {128, 128, 1, 8, 4.3, 4.3, 7.4, 8.0},
-                               {64, 128, 2, 8, 5.9, 3.3, 7.6, 5.5},
-                               {64, 256, 1, 8, 5.6, 4.9, 7.9, 8.1}};
+// than the fastest on average, and more than a tenth at 3 sizes (at most 1.41 times).
+constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.6, 10.4, 0, 0},
+                               {128, 256, 1, 8, 8.0, 6.5, 12.1, 11.1},
+                               {128, 128, 1, 8, 5.0, 3.9, 8.0, 7.2},
+                               {64, 128, 2, 8, 6.0, 3.2, 8.3, 4.7},
+                               {64, 256, 1, 8, 5.7, 5.1, 8.9, 7.0}};
 constexpr int kTileVariants = 5;
 constexpr int kCus = 256;
 constexpr int kTeamMaxM = 32;
@@ -906,7 +906,7 @@ void launch_few_rows(const Fp8BlockPlan& p, const Fp8Product& a, hipStream_t str
 //    32 x 36864 x 7168   87     66            58.2
 // (From 33 rows tiles: 48 x 8192 x 7168 17.7 in tiles of 64 x 128 split four ways, 19.0
 // by the best team.)
-// Tiles: 5 us, then rounds of workgroups at the fitted cost per code, but no faster than
+// Tiles: 4.6 us (7.0 by the bf16 instruction), then rounds of workgroups at the fitted cost per code, but no faster than
 // W comes; a split adds the reduction's launch and its traffic.
 Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide) {
     if (M <= kTeamMaxM) {
@@ -914,7 +914,7 @@ Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide) {
         const int rt = wgs <= kCus ? 1 : 2, waves = wgs <= 2 * kCus ? 8 : 4;
         return Fp8BlockPlan{Fp8BlockPlan::kTeam, M <= 16 ? 1 : 2, rt, waves, 0, 1, K, 0, true};
     }
-    const double stream = (double)N * K / (wide ? 4.1e6 : 9.1e6);
+    const double stream = (double)N * K / (wide ? 4.4e6 : 9.5e6);
     Fp8BlockPlan best{};
     double least = 1e30;
     for (int v = wide ? 1 : 0; v < kTileVariants; ++v) {
@@ -927,9 +927,9 @@ Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide) {
             const int64_t wgs = tiles * S, slots = (int64_t)kCus * c.per_cu, rem = wgs % slots;
             const double rounds = wgs / slots * full + (rem == 0 ? 0.0 : rem <= kCus ? single : full);
             double est = ceil_div(kc, kBlockK) * kBlockK * rounds / 1000.0;
-            est = 5.0 + (est > stream ? est : stream);
+            est = (wide ? 7.0 : 4.6) + (est > stream ? est : stream);
             const size_t ws = S > 1 ? (size_t)S * tiles * c.bm * c.bn * 4 : 0;
-            if (S > 1) est += 1.9 + 7.2 * S * M * N / 4.0e6;
+            if (S > 1) est += 1.8 + (wide ? 5.0 : 7.4) * S * M * N / 4.0e6;
             if (est < least && ws <= ((size_t)1 << 30)) {
                 least = est;
                 best = Fp8BlockPlan{Fp8BlockPlan::kTile, 0, 0, 0, v, S, kc, ws, wide};
