@@ -185,3 +185,24 @@ def test_binding_refuses_what_the_library_cannot_see():
     for call in calls:
         with pytest.raises((TypeError, ValueError)):
             call()
+
+
+def test_every_planned_form_is_in_the_gpu_tests():
+    """The forms that sizes drawn over the whole range plan are those that the GPU tests' sizes
+    reach, and each listed size plans the form it is listed for."""
+    import random
+
+    from fp8_block_forms import FORMS, form
+
+    for M, N, K, f32, kind in FORMS:
+        assert form(M, N, K, f32) == kind, (M, N, K, f32)
+    reached = {f[4] for f in FORMS}
+    rng = random.Random(1)
+
+    def size(lo, hi):
+        return int(round(lo * (hi / lo) ** rng.random()))
+
+    for _ in range(20000):
+        M, N, K = size(1, 9000), size(1, 131000), 16 * size(1, 4096)
+        for f32 in (True, False):
+            assert form(M, N, K, f32) in reached, (M, N, K, f32, form(M, N, K, f32))

@@ -6,6 +6,7 @@ import torch
 
 import fp8_block_ref as ref
 import skinny_gemm_projection_amd as sg
+from fp8_block_forms import FORMS
 from gpu_common import DEV, announce, counters_delta
 
 pytestmark = [pytest.mark.gpu,
@@ -119,7 +120,7 @@ GEMM = [(1, 1, 16), (1, 40, 16), (1, 129, 112), (1, 1024, 1024), (2, 300, 4128),
         (1000, 2051, 1040), (65, 8195, 400), (129, 6147, 1040), (400, 16390, 144)]
 
 
-@pytest.mark.parametrize("M,N,K", GEMM)
+@pytest.mark.parametrize("M,N,K", GEMM + list(dict.fromkeys(f[:3] for f in FORMS)))
 def test_gemm(M, N, K):
     announce(f"fp8_block M={M} N={N} K={K}")
     make = ref.any_codes if (M + N) % 3 == 0 else ref.rand_codes
