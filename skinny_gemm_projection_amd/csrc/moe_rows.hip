@@ -322,6 +322,8 @@ __global__ __launch_bounds__(kBlock) void moe_combine_kernel(
     const int64_t at = (int64_t)blockIdx.x * kSpan + threadIdx.x * 16;
     const int limit = T * topk;
     if (t >= T || at >= pitch) return;
+    // requested with the rows, not behind their sum
+    const uint4 res = load16(make_rsrc(r + (r ? t : 0) * pitch, r ? (uint32_t)pitch : 0u), (uint32_t)at);
     float acc[P::N] = {};
     for (int j0 = 0; j0 < topk; j0 += kAtOnce) {
         uint4 v[kAtOnce];
@@ -346,7 +348,7 @@ __global__ __launch_bounds__(kBlock) void moe_combine_kernel(
     }
     if (r) {
         float y[P::N];
-        P::unpack(*reinterpret_cast<const uint4*>(r + t * pitch + at), y);
+        P::unpack(res, y);
 #pragma unroll
         for (int k = 0; k < P::N; ++k) acc[k] = y[k] + acc[k];
     }
