@@ -260,6 +260,14 @@ __global__ __launch_bounds__(kBlock) void moe_place_kernel(const int32_t* __rest
 
 // ------------------------------------------------------------------ rows
 
+// Rows by expert are read once and written once, and there are topk of them to a token's
+// own: they pass the caches by (non-temporal), which keep the rest.  4099 x 8 x 7168 laid
+// out 122 -> 111 us, back 115 -> 111; both gradients of 2050 x 8 x 7168 162 -> 145.
+__device__ __forceinline__ void store16_nt(char* to, const uint4 v) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(to));
+}
+
 constexpr int kSpan = kBlock * 16;  // bytes of a row a workgroup takes at once
 
 // Workgroups (span, token): tokens go over y and z, whose sizes a launch limits.
@@ -280,7 +288,7 @@ __global__ __launch_bounds__(kBlock) void moe_gather_kernel(const char* __restri
     const uint4 v = *reinterpret_cast<const uint4*>(x + t * pitch + at);
     for (int j = 0; j < topk; ++j) {
         const int pos = positions[t * topk + j];
-        if (pos >= 0 && pos < limit) *reinterpret_cast<uint4*>(rows + pos * pitch + at) = v;
+        if (pos >= 0 && pos < limit) store16_nt(rows + pos * pitch + at, v);
     }
 }
 
@@ -335,7 +343,7 @@ __global__ __launch_bounds__(kBlock) void moe_combine_kernel(
             const bool on = pos >= 0 && pos < limit;
             f[i] = on ? w ? w[t * topk + j] : 1.0f : 0.0f;
             // a left-out pair reads zeros through an empty buffer: no branch around a load
-            v[i] = load16(make_rsrc(rows + (on ? pos : 0) * pitch, on ? (uint32_t)pitch : 0u),
+            v[i] = load16<kStream>(make_rsrc(rows + (on ? pos : 0) * pitch, on ? (uint32_t)pitch : 0u),
                           (uint32_t)at);
         }
 #pragma unroll
@@ -387,7 +395,7 @@ __global__ __launch_bounds__(kBlock) void moe_combine_grad_kernel(
             uint4 v[kAtOnce];
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i)
-                v[i] = load16(make_rsrc(rows + base[i], on[i] ? (uint32_t)pitch : 0u), (uint32_t)at);
+                v[i] = load16<kStream>(make_rsrc(rows + base[i], on[i] ? (uint32_t)pitch : 0u), (uint32_t)at);
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
                 if (!on[i]) continue;
@@ -398,7 +406,7 @@ __global__ __launch_bounds__(kBlock) void moe_combine_grad_kernel(
                     dot[i] = fmaf(g[k], y[k], dot[i]);
                     d[k] = f[i] * g[k];
                 }
-                *reinterpret_cast<uint4*>(d_rows + base[i] + at) = P::pack(d);
+                store16_nt(d_rows + base[i] + at, P::pack(d));
             }
         }
 #pragma unroll
