@@ -20,14 +20,14 @@ __device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true));
 }
 
-template <bool F32>
+template <bool F32, int POLICY>
 __device__ __forceinline__ void load8(const rsrc_t rs, uint32_t piece, float (&v)[8]) {
     if constexpr (F32) {
-        const uint4 a = load16(rs, piece * 32u), b = load16(rs, piece * 32u + 16u);
+        const uint4 a = load16<POLICY>(rs, piece * 32u), b = load16<POLICY>(rs, piece * 32u + 16u);
         v[0] = as_f(a.x), v[1] = as_f(a.y), v[2] = as_f(a.z), v[3] = as_f(a.w);
         v[4] = as_f(b.x), v[5] = as_f(b.y), v[6] = as_f(b.z), v[7] = as_f(b.w);
     } else {
-        const uint4 u = load16(rs, piece * 16u);
+        const uint4 u = load16<POLICY>(rs, piece * 16u);
         const uint32_t d[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -35,6 +35,14 @@ __device__ __forceinline__ void load8(const rsrc_t rs, uint32_t piece, float (&v
             v[2 * i + 1] = as_f(d[i] & 0xffff0000u);
         }
     }
+}
+
+template <bool CACHED>
+__device__ __forceinline__ void store_codes(uint8_t* to, const uint2 c) {
+    if constexpr (CACHED)
+        *reinterpret_cast<uint2*>(to) = c;
+    else
+        __builtin_nontemporal_store(__builtin_bit_cast(uint64_t, c), reinterpret_cast<uint64_t*>(to));
 }
 
 // A wave takes 512 columns (8 a lane, so 16 lanes share a block) of R rows.
@@ -50,13 +58,16 @@ __global__ __launch_bounds__(kBlock) void quant_fp8_kernel(const char* __restric
     const int lane = threadIdx.x & (kWave - 1);
     const int piece = span * kWave + lane;  // of 8 columns
     const int64_t half = (int64_t)K * (F32 ? 4 : 2), pitch = half * (GATED ? 2 : 1);
+    // Of many rows values and codes pass the caches by: 8191 x 7168 bf16 34.9 -> 30.7 us
+    // (the values alone 31.5).
+    constexpr int kPolicy = R > 1 ? kStream : kCached;
     float t[R][8], u[GATED ? R : 1][8];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const uint32_t bytes = r0 + i < M ? (uint32_t)half : 0u;
         const char* row = x + (r0 + i) * pitch;
-        load8<F32>(make_rsrc(row, bytes), piece, t[i]);
-        if constexpr (GATED) load8<F32>(make_rsrc(row + half, bytes), piece, u[i]);
+        load8<F32, kPolicy>(make_rsrc(row, bytes), piece, t[i]);
+        if constexpr (GATED) load8<F32, kPolicy>(make_rsrc(row + half, bytes), piece, u[i]);
     }
     float unit[R];
 #pragma unroll
@@ -74,9 +85,9 @@ __global__ __launch_bounds__(kBlock) void quant_fp8_kernel(const char* __restric
         const BlockScale s = block_scale(amax);
         unit[i] = s.unit;
         if (piece * 8 < K && r0 + i < M)
-            *reinterpret_cast<uint2*>(codes + (r0 + i) * K + piece * 8) =
-                make_uint2(codes4(t[i][0], t[i][1], t[i][2], t[i][3], s),
-                           codes4(t[i][4], t[i][5], t[i][6], t[i][7], s));
+            store_codes<R == 1>(codes + (r0 + i) * K + piece * 8,
+                                make_uint2(codes4(t[i][0], t[i][1], t[i][2], t[i][3], s),
+                                           codes4(t[i][4], t[i][5], t[i][6], t[i][7], s)));
     }
     const int b = span * 4 + (lane >> 4);
     if ((lane & 15) == 0 && b * 128 < K) {
