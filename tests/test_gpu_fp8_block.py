@@ -428,3 +428,27 @@ def test_step_is_its_parts():
         q2, s2 = sg.skinny_quant_fp8(rows)
         u2, _ = sg.grouped_skinny_gemm_fp8(q2, s2, wgu, sgu, offsets)
         assert torch.equal(u, u2), "gathered in the product or before it"
+
+
+@pytest.mark.parametrize("M,N,K", [(33, 129, 144), (131, 1001, 272), (300, 2051, 272), (513, 8229, 144),
+                                   (1030, 8192, 528)])
+def test_bf16_rows_of_any_alignment(M, N, K):
+    """bf16 outputs alone, which leave large products 64 bytes of a row at a time: with a residual,
+    at odd widths, in place, and nothing behind the last element."""
+    announce(f"fp8_block bf16 rows M={M} N={N} K={K}")
+    xq, wq = ref.rand_codes(M, K, 6), ref.rand_codes(N, K, 7)
+    xs, ws = ref.rand_scales((ref.ceil(K), M), 8), ref.rand_scales((ref.ceil(N), ref.ceil(K)), 9)
+    r = normal((M, N), 10)
+    d = [t.to(DEV) for t in (xq, xs, wq, ws)]
+    y, A = ref.product(xq, xs, wq, ws)
+    loose = ref.fp8_rel(K) * A
+    flat = torch.full((M * N + 64,), -7.0, device=DEV, dtype=BF16)
+    out = flat[:M * N].view(M, N)
+    sg.skinny_gemm_fp8_block(*d, y_bf16=out)
+    within(out, y, loose + 2.0 ** -8 * (y.abs() + loose), "plain")
+    out.copy_(r)
+    sg.skinny_gemm_fp8_block(*d, r=out, y_bf16=out)
+    yr = y + r.to(F64)
+    loose = loose + 2 * ref.U * (yr.abs() + loose)
+    within(out, yr, loose + 2.0 ** -8 * (yr.abs() + loose), "residual, in place")
+    assert (flat[M * N:] == -7.0).all(), "behind the last element"
