@@ -97,3 +97,61 @@ def test_fp8_instruction_sums(M, N, K, name, kind):
     cut = 0.125 * cut_sums(x, w)
     off = (got - cut).abs()
     assert (off <= ref.wide_rel(K) * A + own).all(), f"not the cut products: {float((off / A).max()):.3e}"
+
+
+# ------------------------------------------------------------------ fp32's precision
+
+# sizes of every team form, K = 16
+TEAMS = [(5, 901), (1, 4309), (16, 4309), (4, 8999), (23, 241), (32, 6235), (18, 9293)]
+
+
+def cancelling(M, N, seed):
+    """K = 16: 448 * 448 and its negative in two groups of 8, and small products beside them, which
+    the FP8 instruction would lose."""
+    def small(rows, s):
+        return torch.randint(0x30, 0x48, (rows, 16), generator=ref.gen(s), dtype=torch.int32).to(U8)
+
+    xq, wq = small(M, seed), small(N, seed + 1)
+    xq[:, 3], wq[:, 3], xq[:, 12], wq[:, 12] = 0x7e, 0x7e, 0x7e, 0xfe
+    return xq, wq
+
+
+def check_cancelled(out, xq, wq, what):
+    x, w = ref.value(xq), ref.value(wq)
+    y, A = x @ w.t().contiguous(), x.abs() @ w.abs().t().contiguous()
+    # 16 products, the scale, sums of at most 16 parts; an addition may cut
+    bound = (16 + 3 + 16) * 2 * ref.U * A
+    err = (out.cpu().to(F64) - y).abs()
+    assert (err <= bound + 2.0 ** -8 * (y.abs() + bound)).all(), f"{what}: {float(err.max()):.3f}"
+    assert (bound + 2.0 ** -8 * y.abs() < 0.5 * y.abs()).double().mean() > 0.9, "the test can tell"
+
+
+@pytest.mark.parametrize("M,N", TEAMS)
+def test_few_rows_have_fp32_precision(M, N):
+    announce(f"fp8_block cancelling M={M} N={N}")
+    assert form(M, N, 16, False).startswith("team")
+    xq, wq = cancelling(M, N, M + N)
+    one = [torch.ones((1, M), device=DEV), torch.ones((ref.ceil(N), 1), device=DEV)]
+    out = torch.empty((M, N), dtype=BF16, device=DEV)
+    sg.skinny_gemm_fp8_block(xq.to(DEV), one[0], wq.to(DEV), one[1], y_bf16=out)
+    check_cancelled(out, xq, wq, "bf16 alone")
+
+
+@pytest.mark.parametrize("sizes", [[5, 0, 1, 9], [0, 0, 20, 0], [1, 1, 1, 1]])
+@pytest.mark.parametrize("gather", [False, True])
+def test_few_rows_an_expert_have_fp32_precision(sizes, gather):
+    """Up to 5 rows an expert on average, whatever one of them has."""
+    E, N, rows = 4, 300, 20
+    offsets = torch.tensor([0] + torch.tensor(sizes).cumsum(0).tolist(), dtype=torch.int32)
+    X = 7 if gather else rows
+    xq, wq = cancelling(X, E * N, 3)
+    wq = wq.view(E, N, 16)
+    pairs = torch.arange(rows, dtype=torch.int32) % X
+    kw = dict(sorted_pairs=pairs.to(DEV)) if gather else {}
+    out = torch.full((rows, N), -7.0, dtype=BF16, device=DEV)
+    sg.grouped_skinny_gemm_fp8(xq.to(DEV), torch.ones((1, X), device=DEV), wq.to(DEV),
+                               torch.ones((E, 3, 1), device=DEV), offsets.to(DEV), y_bf16=out, **kw)
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        if hi > lo:
+            check_cancelled(out[lo:hi], xq[pairs[lo:hi].long()] if gather else xq[lo:hi], wq[e], f"expert {e}")
