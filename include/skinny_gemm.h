@@ -437,10 +437,13 @@ sg_status skinny_mlp_int8_step(const sg_mlp_int8_step* step, void* workspace,
 sg_status skinny_quant_fp8(int32_t M, int32_t K, const sg_bf16* x_bf16, const float* x_f32,
                            int32_t gated, uint8_t* codes, float* scales, void* stream);
 
-/* y[m,n] = sum_b (sum_{k in block b} x_codes[m,k] W_codes[n,k]) * x_scales[b][m] *
- * W_scales[n/128][b], in fp32.  y_f32 and/or y_bf16 [M, N] (at least one); r
+/* y[m,n] = sum_b (sum_{k in block b} x_codes[m,k] W_codes[n,k]) * (x_scales[b][m] *
+ * W_scales[n/128][b]), in fp32.  y_f32 and/or y_bf16 [M, N] (at least one); r
  * (nullable) bf16 [M, N] gives the fused residual out = r + y, rounded once;
  * y_bf16 may equal r.  A NaN code or scale makes its outputs NaN.
+ * Scales: a block's two are multiplied first, rounded once.  Where their product
+ * leaves fp32's normal range it behaves as fp32 does: past 2^128 it is an infinity
+ * (NaN against a sum of 0), below 2^-126 it keeps fewer bits.
  * Sums: with y_f32, and up to 32 rows, every product and sum is at fp32's
  * precision.  With y_bf16 alone and more rows a block's sum is taken by the
  * matrix cores' FP8 instruction, which cuts each 8 neighbouring products to 13 bits

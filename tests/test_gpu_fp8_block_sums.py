@@ -155,3 +155,88 @@ def test_few_rows_an_expert_have_fp32_precision(sizes, gather):
         lo, hi = int(offsets[e]), int(offsets[e + 1])
         if hi > lo:
             check_cancelled(out[lo:hi], xq[pairs[lo:hi].long()] if gather else xq[lo:hi], wq[e], f"expert {e}")
+
+
+# ------------------------------------------------------------------ scales of any size
+
+X_SCALES = [2.0 ** -126, 2.0 ** -70 * 1.37, 1.1, 2.0 ** 62 * 1.5, 2.0 ** -149]
+W_SCALES = [2.0 ** -80 * 1.13, 0.9, 2.0 ** 66 * 1.3]
+
+
+def check_scaled(out, xq, xs, wq, ws, rel, dtype, what):
+    """Against sum_b S_b (xs_b ws_b) with the scales' product rounded to fp32 as the interface says;
+    no sum of these inputs overflows but by that product."""
+    y, A = torch.zeros(out.shape, dtype=F64), torch.zeros(out.shape, dtype=F64)
+    for b in range(xs.shape[0]):
+        k = slice(128 * b, 128 * b + 128)
+        x, w = ref.value(xq[:, k]), ref.value(wq[:, k])
+        f = (xs[b][:, None] * ws[:, b].repeat_interleave(128)[None, :wq.shape[0]]).to(F64)
+        y += x @ w.t().contiguous() * f
+        A += torch.where(torch.isfinite(f), x.abs() @ w.abs().t().contiguous() * f, 0.0)
+    out = out.cpu().to(F64)
+    for name, test in (("NaN", torch.isnan), ("+inf", torch.isposinf), ("-inf", torch.isneginf)):
+        assert torch.equal(test(out), test(y)), f"{what}: {name}"
+    ok = torch.isfinite(y)
+    bound = rel * A + (xs.shape[0] + 20) * 2.0 ** -149  # subnormal sums round to multiples of 2^-149
+    if dtype is BF16:
+        bound = bound + 2.0 ** -8 * (y.abs() + bound) + 2.0 ** -134
+    err = (out - y).abs()
+    assert (err <= bound)[ok].all(), f"{what}: {float((err - bound)[ok].max()):.3e}"
+
+
+def scaled_inputs(M, N, K, E=1):
+    """Rows and blocks of channels with every pair of scales; some rows and channels of zeros."""
+    xq, wq = ref.rand_codes(M, K, 1), ref.rand_codes(E * N, K, 2)
+    xq[::4], wq[::9] = 0, 0
+    kb, nb = ref.ceil(K), ref.ceil(N)
+    xs = torch.tensor(X_SCALES)[torch.arange(M) % 5].repeat(kb, 1)
+    ws = torch.tensor(W_SCALES)[torch.arange(E * nb) % 3].view(E, nb, 1).repeat(1, 1, kb)
+    return xq, xs, wq.view(E, N, K), ws
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", [(5, 901, 272), (23, 400, 128), (40, 700, 288), (95, 649, 8176),
+                                   (300, 1030, 400), (1200, 800, 144)])
+def test_scales_of_any_size(M, N, K, dtype):
+    announce(f"fp8_block scales M={M} N={N} K={K} {dtype}")
+    xq, xs, wq, ws = scaled_inputs(M, N, K)
+    out = torch.empty((M, N), dtype=dtype, device=DEV)
+    sg.skinny_gemm_fp8_block(xq.to(DEV), xs.to(DEV), wq[0].to(DEV), ws[0].to(DEV),
+                             **{"y_f32" if dtype is F32 else "y_bf16": out})
+    # random codes of these sigmas lose far less than the bound to their subnormals
+    rel = ref.fp8_rel(K) if dtype is BF16 and M > 32 else ref.wide_rel(K)
+    check_scaled(out, xq, xs, wq[0], ws[0], rel, dtype, f"{M} x {N} x {K}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [12, 90, 700])
+def test_scales_of_any_size_by_expert(rows, dtype):
+    E, N, K = 3, 400, 272
+    xq, xs, wq, ws = scaled_inputs(rows, N, K, E)
+    offsets = torch.tensor([0, rows // 3, rows // 3, rows], dtype=torch.int32)
+    out = torch.empty((rows, N), dtype=dtype, device=DEV)
+    sg.grouped_skinny_gemm_fp8(*[t.to(DEV) for t in (xq, xs, wq, ws, offsets)],
+                               **{"y_f32" if dtype is F32 else "y_bf16": out})
+    rel = ref.fp8_rel(K) if dtype is BF16 and rows > 12 else ref.wide_rel(K)
+    for e in (0, 2):
+        s = slice(int(offsets[e]), int(offsets[e + 1]))
+        check_scaled(out[s], xq[s], xs[:, s], wq[e], ws[e], rel, dtype, f"expert {e}")
+
+
+@pytest.mark.parametrize("T", [3, 100])
+def test_quantised_rows_of_zeros_and_small_weight_scales(T):
+    """A block of zeros has the scale 2^-126: its product with a weight's scale is subnormal, its
+    outputs are zeros."""
+    x = normal_rows(T, 272)
+    x[0], x[T - 1, 128:] = 0, 0
+    q, s = sg.skinny_quant_fp8(x.to(DEV))
+    assert float(s[0, 0]) == 2.0 ** -126
+    wq, ws = ref.rand_codes(70, 272, 2), ref.rand_scales((1, 3), 3) * 2.0 ** -20
+    y, _ = sg.skinny_gemm_fp8_block(q, s, wq.to(DEV), ws.to(DEV))
+    assert (y[0] == 0).all()
+    want, A = ref.product(q.cpu(), s.cpu(), wq, ws)
+    assert ((y.cpu().to(F64) - want).abs() <= ref.wide_rel(272) * A + 2.0 ** -145).all()
+
+
+def normal_rows(T, K):
+    return torch.randn((T, K), generator=ref.gen(T)).to(BF16)
