@@ -409,6 +409,12 @@ struct Fp8Tile {
     static constexpr int kWScales = BN > kBlockK ? BN / kBlockK : 1;
 };
 
+// Workgroups of a tile kernel go over x and, past kGridX of them, z: the threads of one
+// dimension are counted in 32 bits.  x is a multiple of 8, so a workgroup's number
+// modulo 8 still says its XCD.
+constexpr int kGridX = 1 << 16;
+__device__ __forceinline__ int workgroup() { return (int)(blockIdx.z * gridDim.x + blockIdx.x); }
+
 template <class T, int OUT, bool GROUPED, bool WIDE>
 __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kernel(
     Fp8Product a, int tiles, int per_xcd, int group, int kc, float* partial) {
@@ -458,8 +464,8 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
             a.offsets, a.E, a.M, [](int n) { return (n + BM - 1) / BM; },
             [&](int units) {
                 const int total = units * nn, per = (total + kXcds - 1) / kXcds;
-                const int slot = blockIdx.x / kXcds;
-                t = (int)(blockIdx.x % kXcds) * per + slot;
+                const int wg = workgroup(), slot = wg / kXcds;
+                t = wg % kXcds * per + slot;
                 return slot < per && t < total ? t / nn : -1;
             },
             &v, &first);
@@ -473,8 +479,9 @@ __global__ __launch_bounds__(T::W* kWave, T::W == 8 ? 2 : 1) void fp8_tile_kerne
         // Workgroups reach the 8 XCDs in turn: each XCD takes a run of consecutive
         // tiles, and a run goes down `group` tiles of x before the next tile of W, so
         // the tiles in flight on an XCD share rows of both through its L2.
-        t = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
-        if (t >= tiles) return;
+        const int wg = workgroup();
+        t = wg % kXcds * per_xcd + wg / kXcds;
+        if (wg / kXcds >= per_xcd || t >= tiles) return;
         const int nm = (a.M + BM - 1) / BM;
         const int first = t / (group * nn) * group, in = t - first * nn;
         const int rows = min(group, nm - first);
@@ -880,11 +887,17 @@ constexpr int kTileVariants = 5;
 constexpr int kCus = 256;
 constexpr int kTeamMaxM = 32;
 
+// At least wgs workgroups, fewer than 8 too many for each layer of z.
+dim3 tile_grid(int64_t wgs, int S) {
+    const int64_t z = ceil_div(wgs, kGridX);
+    return dim3((uint32_t)(ceil_div(ceil_div(wgs, z), kXcds) * kXcds), (uint32_t)S, (uint32_t)z);
+}
+
 template <class T, int OUT, bool WIDE>
 void launch_tiles(const Fp8Product& a, int S, int kc, int group, float* partial, hipStream_t stream) {
     const int tiles = (int)(ceil_div(a.M, T::BM) * ceil_div(a.N, T::BN));
     const int per = (int)ceil_div(tiles, kXcds);
-    hipLaunchKernelGGL((fp8_tile_kernel<T, OUT, false, WIDE>), dim3(per * kXcds, S),
+    hipLaunchKernelGGL((fp8_tile_kernel<T, OUT, false, WIDE>), tile_grid((int64_t)per * kXcds, S),
                        dim3(T::W * kWave), 0, stream, a, tiles, per, group, kc, partial);
 }
 
@@ -912,8 +925,8 @@ template <class T, int OUT, bool WIDE>
 void launch_grouped_tiles(const Fp8Product& a, hipStream_t stream) {
     const int64_t tiles = most_tiles<T>(a.M, a.E, OUT == kTileGated ? 2 * a.N : a.N);
     hipLaunchKernelGGL((fp8_tile_kernel<T, OUT, true, WIDE>),
-                       dim3((uint32_t)(ceil_div(tiles, kXcds) * kXcds)), dim3(T::W * kWave), 0, stream, a,
-                       0, 0, 0, a.K, nullptr);
+                       tile_grid(ceil_div(tiles, kXcds) * kXcds, 1), dim3(T::W * kWave), 0, stream, a, 0, 0,
+                       0, a.K, nullptr);
 }
 
 template <int S, int RT, int MT, bool GROUPED>
@@ -1002,16 +1015,6 @@ bool fp8_gated_ok(const Fp8BlockPlan& p, int F) {
     if (p.kind == Fp8BlockPlan::kTile && !p.wide)
         with_tile(p.tile, [&](auto shape) { ok = decltype(shape)::BN == 2 * kBlockK; });
     return ok && F % kBlockK == 0;
-}
-
-bool fp8_grouped_fits(const Fp8BlockPlan& p, int M, int E, int N) {
-    if (p.kind == Fp8BlockPlan::kTeam) return true;
-    bool fits = false;
-    with_tile(p.tile, [&](auto shape) {  // threads of a launch are counted in 32 bits
-        typedef decltype(shape) T;
-        fits = (most_tiles<T>(M, E, N) + kXcds) * T::W * kWave < ((int64_t)1 << 32);
-    });
-    return fits;
 }
 
 hipError_t launch_fp8_block(const Fp8BlockPlan& p, const Fp8Product& product, void* ws,

@@ -235,7 +235,6 @@ sg_status grouped_skinny_gemm_fp8(int32_t rows, int32_t x_rows, int32_t E, int32
         !aligned(y_f32, 16) || !aligned(y_bf16, 16))
         return SG_ERR_ALIGN;
     const sg::Fp8BlockPlan plan = sg::fp8_grouped_plan(rows, E, N, K, y_f32 != nullptr);
-    if (!sg::fp8_grouped_fits(plan, rows, E, N)) return SG_ERR_SHAPE;
     sg::Fp8Product a{x_codes, x_scales, W_codes, W_scales, rows, N, K, x_rows, y_f32, y_bf16, nullptr};
     a.offsets = expert_offsets, a.E = E, a.pairs = sorted_pairs, a.topk = topk;
     return product(plan, a, nullptr, static_cast<hipStream_t>(stream));
@@ -263,8 +262,6 @@ sg_status skinny_moe_fp8_step(const sg_moe_fp8_step* a, void* workspace, size_t 
         !aligned(a->W_gate_up, 16) || !aligned(a->W_down, 16) || !aligned(a->topk_ids, 4) ||
         !aligned(a->topk_weights, 4) || !aligned(a->gate_up_scales, 4) || !aligned(a->down_scales, 4))
         return SG_ERR_ALIGN;
-    if (!sg::fp8_grouped_fits(L.up, P, E, 2 * F) || !sg::fp8_grouped_fits(L.down, P, E, H))
-        return SG_ERR_SHAPE;
     if (!workspace || workspace_bytes < L.total) return SG_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return SG_ERR_ALIGN;
 

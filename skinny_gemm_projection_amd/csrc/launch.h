@@ -265,7 +265,6 @@ Fp8BlockPlan fp8_grouped_plan(int M, int E, int N, int K, bool wide);
 // Whether a grouped product of 2F gate and up rows by this plan can give the gated
 // product's codes itself (Fp8Product::codes, N = F).
 bool fp8_gated_ok(const Fp8BlockPlan& p, int F);
-bool fp8_grouped_fits(const Fp8BlockPlan& p, int M, int E, int N);  // in one launch's limits
 hipError_t launch_fp8_block(const Fp8BlockPlan& p, const Fp8Product& a, void* ws, hipStream_t stream);
 
 // Router top-k: ids [T,k] (and their scores) from fp32 scores, row t at
