@@ -107,6 +107,7 @@ __device__ __forceinline__ void place_pairs(const int32_t* __restrict__ ids, int
 }
 
 constexpr int kSortMaxExperts = 4096;
+constexpr int kSortManyWavesExperts = 1024;  // 16 waves in one workgroup: their counts take 68 KB
 constexpr int kSortOneMax = 4096;      // pairs one workgroup sorts alone
 constexpr int kSortChunk = 1024;       // pairs of a workgroup beyond, in two launches,
 constexpr int kSortTwoMax = 1 << 16;   // up to so many pairs
@@ -448,14 +449,17 @@ size_t moe_sort_workspace_bytes(int64_t P, int E) {
     return (size_t)(std::max(small, big) + 1) * E * 4;
 }
 
-// One of the sorting kernels, each with `ints` ints of LDS.
+// One of the sorting kernels, with `per` ints of LDS for each of E experts.  The limit set is
+// the kernel's own for as many experts as it takes, the same in every call: it belongs to
+// the kernel, and a call for fewer experts may come between another thread's two steps.
 template <class... P, class... A>
-static hipError_t launch_sort(void (*kernel)(P...), int grid, int block, size_t ints, hipStream_t stream,
-                              A... args) {
+static hipError_t launch_sort(void (*kernel)(P...), int grid, int block, int per, int most_experts, int E,
+                              hipStream_t stream, A... args) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)(ints * 4));
+                                             hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             per * most_experts * 4);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), ints * 4, stream, args...);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), (size_t)per * E * 4, stream, args...);
     return hipGetLastError();
 }
 
@@ -464,29 +468,29 @@ hipError_t launch_moe_sort(const int32_t* ids, int P, int E, int32_t* offsets, i
     int bits = 0;
     while ((1 << bits) < E) ++bits;
     if (P <= kSortOneMax) {
-        // 16 waves while their counts take at most 68 KB of LDS, and are needed
-        if (E <= 1024 && P > 4 * kWave)
-            return launch_sort(moe_sort_one_kernel<16>, 1, 16 * kWave, (size_t)17 * E, stream, ids, P, E,
-                               bits, offsets, sorted, positions);
-        return launch_sort(moe_sort_one_kernel<4>, 1, 4 * kWave, (size_t)5 * E, stream, ids, P, E, bits,
-                           offsets, sorted, positions);
+        // 16 waves while their counts fit, and are needed
+        if (E <= kSortManyWavesExperts && P > 4 * kWave)
+            return launch_sort(moe_sort_one_kernel<16>, 1, 16 * kWave, 17, kSortManyWavesExperts, E, stream,
+                               ids, P, E, bits, offsets, sorted, positions);
+        return launch_sort(moe_sort_one_kernel<4>, 1, 4 * kWave, 5, kSortMaxExperts, E, stream, ids, P, E,
+                           bits, offsets, sorted, positions);
     }
     const bool two = moe_sort_launches(P, E) == 2;
     const int chunk = two ? kSortChunk : kSortBigChunk, chunks = (P + chunk - 1) / chunk;
-    const size_t ints = (size_t)(kWavesPerBlock + 2) * E;
+    constexpr int kPer = kWavesPerBlock + 2;
     int32_t* counts = static_cast<int32_t*>(ws);
     int32_t* totals = counts + (int64_t)chunks * E;
     hipLaunchKernelGGL(moe_count_kernel, dim3(chunks), dim3(kBlock), 0, stream, ids, P, chunk, E, counts);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (two)
-        return launch_sort(moe_place_kernel<false>, chunks, kBlock, ints, stream, ids, P, chunk, chunks, E,
-                           bits, counts, totals, offsets, sorted, positions);
+        return launch_sort(moe_place_kernel<false>, chunks, kBlock, kPer, kSortMaxExperts, E, stream, ids, P,
+                           chunk, chunks, E, bits, counts, totals, offsets, sorted, positions);
     hipLaunchKernelGGL(moe_scan_kernel, dim3((E + kWave - 1) / kWave), dim3(kWave), 0, stream, counts,
                        chunks, E, totals);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    return launch_sort(moe_place_kernel<true>, chunks, kBlock, ints, stream, ids, P, chunk, chunks, E, bits,
-                       counts, totals, offsets, sorted, positions);
+    return launch_sort(moe_place_kernel<true>, chunks, kBlock, kPer, kSortMaxExperts, E, stream, ids, P,
+                       chunk, chunks, E, bits, counts, totals, offsets, sorted, positions);
 }
 
 hipError_t launch_moe_gather(const void* x, int T, int topk, int64_t pitch, const int32_t* positions,
