@@ -468,12 +468,14 @@ hipError_t launch_lowp_chunk(int fmt, int M, int N, int K, const void* x, const 
     // 16.00 us).
     const int wpw = p.chunk / kLpWindow;
     const bool all = fmt == kLowpFp8 && p.MT == 1 && p.NT == 1 && (wpw == 7 || wpw == 8);
+    // The kernel's limit is the same in every call (another host thread may launch it for
+    // another size in between).
 #define SG_LP(f, mt, nt, d, a)                                                                    \
     if (fmt == f && p.MT == mt && p.NT == nt && all == a) {                                       \
         auto* kern = &lowp_chunk_kernel<f, mt, nt, d, a>;                                         \
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),                   \
                                            hipFuncAttributeMaxDynamicSharedMemorySize,            \
-                                           (int)p.lds);                                           \
+                                           (int)kLpLdsMax);                                       \
         if (e != hipSuccess) return e;                                                            \
         kern<<<grid, kLpThreads, p.lds, stream>>>(xp, wp, Ws, M, N, K, p.chunk, p.pitch, ep);    \
         e = hipGetLastError();                                                                    \

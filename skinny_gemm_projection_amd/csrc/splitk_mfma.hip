@@ -605,11 +605,13 @@ hipError_t launch_splitk_mfma(int M, int N, int K, int S, int k_chunk, int tile_
     // 14.98 / 15.11 / 18.23 -> 14.07 / 14.18 / 17.00 us, 8192x7168 M = 64
     // 30.33 -> 28.96 us.
     const int rounds = whole / (16 / NT);
+    // A kernel's LDS limit is the same in every call: another host thread may launch the
+    // kernel for another size between the two steps.
 #define SG_CHUNK_R(mt, nt, r) \
     if (MT == mt && NT == nt && !phased && rounds == r) { \
         hipError_t e = hipFuncSetAttribute( \
             reinterpret_cast<const void*>(&splitk_mfma_kernel<mt, nt, DR, false, r>), \
-            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds); \
+            hipFuncAttributeMaxDynamicSharedMemorySize, (int)kMfmaMaxLds); \
         if (e != hipSuccess) return e; \
         splitk_mfma_kernel<mt, nt, DR, false, r><<<grid, kChunkThreads, lds, stream>>>( \
             xp, wp, M, N, K8, chunk8, phase, ep); \
@@ -627,7 +629,7 @@ hipError_t launch_splitk_mfma(int M, int N, int K, int S, int k_chunk, int tile_
     if (MT == mt && NT == nt && phased == ph) { \
         hipError_t e = hipFuncSetAttribute( \
             reinterpret_cast<const void*>(&splitk_mfma_kernel<mt, nt, DR, ph, 0>), \
-            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds); \
+            hipFuncAttributeMaxDynamicSharedMemorySize, (int)kMfmaMaxLds); \
         if (e != hipSuccess) return e; \
         splitk_mfma_kernel<mt, nt, DR, ph, 0><<<grid, kChunkThreads, lds, stream>>>( \
             xp, wp, M, N, K8, chunk8, phase, ep); \

@@ -1,7 +1,8 @@
-// lds_limit_checks.cpp -- the launches of skinny_moe_sort on a host without a GPU: the
-// runtime's calls that set a kernel's dynamic LDS limit and launch it are replaced by
-// records.  A limit is a property of the kernel, shared by every thread that launches
-// it, so no call may set it below what another call's launch takes.
+// lds_limit_checks.cpp -- launches whose LDS depends on the sizes (skinny_moe_sort, and the
+// chunk kernels of skinny_gemm and skinny_gemm_fp8) on a host without a GPU: the runtime's
+// calls that set a kernel's dynamic LDS limit and launch it are replaced by records.  A
+// limit is a property of the kernel, shared by every thread that launches it, so no call
+// may set it below what another call's launch takes.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -54,6 +55,21 @@ int main() {
                 return 1;
             }
         }
+    // the chunk kernels: bf16 rows by bf16 and by block-scaled FP8 weights
+    sg_bf16* b = reinterpret_cast<sg_bf16*>((uintptr_t)4096);
+    float* y = reinterpret_cast<float*>((uintptr_t)4096);
+    for (int32_t M : {64, 9, 12, 17, 33, 48, 64})
+        for (int32_t N : {512, 4096, 8192, 36864})
+            for (int32_t K : {256, 1024, 2048, 4096, 7168, 8192, 16384}) {
+                sg_plan plan;
+                if (skinny_gemm_plan(M, N, K, &plan) != SG_OK ||
+                    skinny_gemm(&plan, b, b, y, nullptr, p, (size_t)1 << 40, nullptr) != SG_OK ||
+                    skinny_gemm_fp8(M, N, K, b, reinterpret_cast<uint8_t*>(b), y, nullptr, y, nullptr, p,
+                                    (size_t)1 << 40, nullptr) != SG_OK) {
+                    std::fprintf(stderr, "%d x %d x %d is refused\n", M, N, K);
+                    return 1;
+                }
+            }
     int bad = 0;
     for (const auto& k : most)
         if (k.second > 0 && (!least.count(k.first) || least[k.first] < k.second)) {

@@ -1,4 +1,4 @@
-"""Launches of skinny_moe_sort from several host threads, without a GPU: see
+"""Launches from several host threads whose LDS depends on the sizes, without a GPU: see
 asan/lds_limit_checks.cpp, which replaces the runtime's launch calls by records."""
 import os
 import subprocess
@@ -12,7 +12,7 @@ SOURCE = os.path.join(ROOT, "tests", "asan", "lds_limit_checks.cpp")
 
 
 @pytest.mark.skipif(not os.path.exists(HIPCC) or not os.path.exists(SOURCE), reason="hipcc or source not found")
-def test_no_sort_lowers_the_limit_of_another(tmp_path):
+def test_no_call_lowers_the_limit_of_another(tmp_path):
     objects = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in build.SOURCES]
     missing = [o for o in objects if not os.path.exists(o)]
     if missing:
