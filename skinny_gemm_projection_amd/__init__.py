@@ -722,6 +722,8 @@ def grouped_skinny_gemm_fp8(x_codes: torch.Tensor, x_scales: torch.Tensor, W_cod
     y_f32 and/or y_bf16 [rows, N]; rows behind the last segment are left as they were (zeros in a
     y_f32 allocated here, which happens when no output is given).  Returns the outputs."""
     u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    if not 0 < topk <= 0x7fffffff:  # the C ABI's sizes are int32 and would wrap around
+        raise ValueError(f"topk: expected a positive number of slots a token, got {topk}")
     X, K, dev, px = _rows(x_codes, "x_codes", (u8,))
     E, N, K2, pw = _experts(W_codes, "W_codes", dev)
     if K2 != K:
@@ -732,6 +734,8 @@ def grouped_skinny_gemm_fp8(x_codes: torch.Tensor, x_scales: torch.Tensor, W_cod
         if not isinstance(sorted_pairs, torch.Tensor):
             raise TypeError(f"sorted_pairs: expected a torch.Tensor, got {type(sorted_pairs).__name__}")
         rows = sorted_pairs.numel()
+        if rows > 0x7fffffff:
+            raise ValueError(f"sorted_pairs: {rows} pairs are past 2^31 - 1")
     if y_f32 is None and y_bf16 is None:
         y_f32 = _new((rows, N), f32, dev, stream)
         with torch.cuda.stream(_as_stream(stream, dev)):
