@@ -476,7 +476,7 @@ size_t skinny_gemm_fp8_block_workspace(int32_t M, int32_t N, int32_t K, int32_t 
  * of a pair among the sorted ones, -1 if it is left out; sorted_pairs [T*topk]
  * (NULL to skip): the pair at each place, ascending in p inside an expert, -1
  * behind the last.  workspace: skinny_moe_sort_workspace bytes (16-byte aligned;
- * NULL when that is 0).
+ * NULL when that is 0).  No buffers may overlap.
  * Limits: 0 <= T, 1 <= topk <= SG_MOE_MAX_TOPK, T * topk <= SG_MOE_MAX_PAIRS, 1 <=
  * E <= SG_MOE_MAX_EXPERTS (else SG_ERR_SHAPE); pointers 4-byte aligned. */
 sg_status skinny_moe_sort(int32_t T, int32_t topk, int32_t E, const int32_t* topk_ids,
@@ -487,8 +487,8 @@ size_t skinny_moe_sort_workspace(int32_t T, int32_t topk, int32_t E);
 /* rows[positions[t][j]] = x[t]: token rows laid out by expert.  x [T, K], rows
  * [T*topk, K], both bf16 (f32 == 0) or fp32 (f32 == 1).  Rows that no position
  * names (behind the last valid pair) are left as they were; a position outside
- * [0, T*topk) is taken as left out.  Its gradient is skinny_moe_combine without
- * weights.
+ * [0, T*topk) is taken as left out.  No buffers may overlap.  Its gradient is
+ * skinny_moe_combine without weights.
  * Limits of this call and the two below: T and topk as for skinny_moe_sort, 1 <= K
  * <= SG_ROW_MAX_K, f32 0 or 1 (else SG_ERR_SHAPE); K % 8 == 0, rows 16-byte and
  * the rest 4-byte aligned (else SG_ERR_ALIGN).  No two pairs may share a
@@ -521,9 +521,12 @@ sg_status skinny_moe_combine_grad(int32_t T, int32_t topk, int32_t K, const void
  * With sorted_pairs x_i is row sorted_pairs[i] / topk of x [x_rows, K] (tokens,
  * gathered as they are read), without (NULL) row i of x [rows, K] (x_rows == rows).
  * y_f32 and/or y_bf16 [rows, N]; rows behind offsets[E] are left as they were.
- * Precision as for skinny_gemm_fp8_block, where few rows an expert count as few
- * rows.  Offsets are clamped to [0, rows]; a gathered row outside [0, x_rows)
- * reads as zeros.
+ * Precision as for skinny_gemm_fp8_block, where up to 5 rows an expert on average
+ * count as few rows.  The average is rows / min(E, rows), in whole rows, and counts
+ * those behind offsets[E] too: the host does not know them.  The kernel's form goes by
+ * it as well, so a rank that holds few of the experts its table names gets the form
+ * for more rows than it has (48 of 384 experts: up to a fifth longer).  Offsets are
+ * clamped to [0, rows]; a gathered row outside [0, x_rows) reads as zeros.
  * Limits: 0 <= rows <= SG_MOE_MAX_PAIRS, 1 <= E <= SG_MOE_MAX_EXPERTS, 0 <= N <=
  * 1<<20, 0 <= K <= SG_FP8_MAX_K, 1 <= topk <= SG_MOE_MAX_TOPK, gathered x_rows * K
  * < 2^31 (else SG_ERR_SHAPE); alignment as for skinny_gemm_fp8_block.  Allocates
@@ -542,6 +545,8 @@ sg_status grouped_skinny_gemm_fp8(int32_t rows, int32_t x_rows, int32_t E, int32
  *       the codes then leave the product itself and u is not stored)
  *   y = p W_down[e]^T, bf16                             (grouped_skinny_gemm_fp8)
  *   out[t] = (r[t] +) sum_j topk_weights[t][j] * y          (skinny_moe_combine)
+ * y is rounded to bf16 (2^-8) once before the weighted sum.  The calls themselves, with
+ * y_f32 in both products and fp32 rows, keep fp32's precision in every sum.
  * x, r, out [T, H] bf16 (r nullable; out may be x's or r's buffer); topk_ids
  * [T, topk] int32 (ids outside [0, E) are left out), topk_weights [T, topk] fp32;
  * W_gate_up [E, 2F, H] (an expert's gate rows, then its up rows) with scales

@@ -876,8 +876,9 @@ struct TileCost {
     double full, single, wide_full, wide_single;
 };
 // Fitted to the times of every form at 198 sizes of 40 to 2049 rows, 700 to 36864
-// channels and 1040 to 16384 codes: the form with the least estimate takes 1 % longer
-// than the fastest on average, and more than a tenth at 3 sizes (at most 1.41 times).
+// channels and 1040 to 16384 codes.  At 110 other sizes (33 to 4096 rows) the form with
+// the least estimate takes 1.3 % longer than the fastest on average with bf16 outputs and
+// 2.3 % with fp32 ones, and more than a tenth at 5 sizes each (at most 1.21 and 1.52 times).
 constexpr TileCost kTiles[] = {{256, 256, 1, 4, 12.6, 10.4, 0, 0},
                                {128, 256, 1, 8, 8.0, 6.5, 12.1, 11.1},
                                {128, 128, 1, 8, 5.0, 3.9, 8.0, 7.2},
@@ -999,9 +1000,23 @@ Fp8BlockPlan fp8_block_plan(int M, int N, int K, bool wide) {
 
 // Few rows an expert: teams of 2 waves, 6 workgroups a compute unit, so that one's look
 // for its expert is hidden behind the others' streams (experts of 4 tokens, 1 GB: 174 us
-// the step against 266 with 8 waves, 180 with 4).  From 6 rows on average tiles of 64
-// rows, which also bound what one popular expert costs (48 experts, 64 tokens of 8: 374
-// us against 431; 32 tokens 361 against 334).
+// the step against 266 with 8 waves, 180 with 4).  Both products, us, by rows an expert on
+// average (48 experts of 7168 and 2048 | 64 of 4096 and 1408; some experts more popular):
+//      rows   team        64x256      128x256     256x256
+//         4   303 | 160   345 | 202   351 | 204   402 | 225
+//         6   332 | 188   352 | 215   356 | 218   406 | 243
+//        12   438 | 273   372 | 217   377 | 226   428 | 249
+//        32   941 | 563   411 | 267   398 | 251   452 | 276
+//        64               478 | 305   453 | 292   473 | 292
+//       128               664 | 375   538 | 325   575 | 347
+//       160               724 | 427   608 | 357   593 | 358
+//       334              1272 | 727   998 | 561   899 | 507
+// The team walks an expert's rows 16 at a time, its weights anew each time: tiles from 6
+// rows on, a little early, bound what a crowd costs (240 rows, 120 of them one expert's:
+// 292 us the first product, tiles 282; all 200 of 200: 194 and 37).  N and K move these
+// crossings little.  The average counts rows that are left out, which only the device
+// knows: 48 of 384 experts held, 64 tokens of 8 take 187 us in tiles, a team would 155;
+// 2003 tokens 459 in 256 x 256, 408 in 128 x 256.
 Fp8BlockPlan fp8_grouped_plan(int M, int E, int N, int K, bool wide) {
     (void)N;
     const int64_t rows = M / (E < M ? E : M);  // an expert's, on average

@@ -84,7 +84,8 @@ bool step_layout(int32_t T, int32_t topk, int32_t E, int32_t H, int32_t F, StepL
     };
     const size_t P = (size_t)T * topk, t = (size_t)T;
     const int rows = P > 0 ? (int)P : 1;
-    // what follows is rounded to 4 bits: the FP8 instruction's sums do
+    // What follows is rounded to 4 bits, 2^-4 of a value: the FP8 instruction's sums do (with
+    // fp32's the gate and up product of 2003 tokens, 48 experts, takes 1026 us, not 582).
     L->up = sg::fp8_grouped_plan(rows, E, 2 * F, H, false);
     L->gated = sg::fp8_gated_ok(L->up, F);
     L->down = sg::fp8_grouped_plan(rows, E, H, F, false);
@@ -285,7 +286,9 @@ sg_status skinny_moe_fp8_step(const sg_moe_fp8_step* a, void* workspace, size_t 
     if (L.gated) up.N = F, up.y_f32 = nullptr, up.codes = p, up.scales = sp;
     if ((st = product(L.up, up, nullptr, hs)) != SG_OK) return st;
     if (!L.gated && (st = quant(P, F, u, true, true, p, sp, hs)) != SG_OK) return st;
-    // the rows of y are bf16: one rounding each before the weighted sum
+    // The rows of y are bf16, one rounding of 2^-8 each before the weighted sum in fp32, as
+    // large as the output's own: product and sum of 2003 tokens, 48 experts, take 370 us, with
+    // fp32 rows 446 and twice the workspace.
     sg::Fp8Product down{p, sp, a->W_down, a->down_scales, P, H, F, P, nullptr, y, nullptr};
     down.offsets = offsets, down.E = E;
     if ((st = product(L.down, down, nullptr, hs)) != SG_OK) return st;
