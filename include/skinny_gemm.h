@@ -543,10 +543,11 @@ sg_status grouped_skinny_gemm_fp8(int32_t rows, int32_t x_rows, int32_t E, int32
  *   p = codes of silu(u[:, :F]) * u[:, F:]                     (skinny_quant_fp8)
  *       (for many rows an expert the FP8 instruction's sums; where F % 128 == 0
  *       the codes then leave the product itself and u is not stored)
- *   y = p W_down[e]^T, bf16                             (grouped_skinny_gemm_fp8)
- *   out[t] = (r[t] +) sum_j topk_weights[t][j] * y          (skinny_moe_combine)
- * y is rounded to bf16 (2^-8) once before the weighted sum.  The calls themselves, with
- * y_f32 in both products and fp32 rows, keep fp32's precision in every sum.
+ *   y = p W_down[e]^T, fp32                             (grouped_skinny_gemm_fp8)
+ *   out[t] = (r[t] +) sum_j topk_weights[t][j] * y, rounded once
+ *                                                            (skinny_moe_combine)
+ * From 6 rows an expert on average both products take the FP8 instruction's sums (see
+ * skinny_gemm_fp8_block); the calls themselves with y_f32 keep fp32's precision in them.
  * x, r, out [T, H] bf16 (r nullable; out may be x's or r's buffer); topk_ids
  * [T, topk] int32 (ids outside [0, E) are left out), topk_weights [T, topk] fp32;
  * W_gate_up [E, 2F, H] (an expert's gate rows, then its up rows) with scales

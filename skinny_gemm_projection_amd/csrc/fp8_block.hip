@@ -349,8 +349,8 @@ __global__ __launch_bounds__(S* kWave) void fp8_team_kernel(Fp8Product a) {
 // bf16 outputs of two neighbouring 16-channel tiles, whose channels 4 * grp .. a lane holds
 // in ya and yb: lanes 16 apart trade halves, so that each has 8 neighbours of one tile
 // and a row's 32 channels are one 64-byte run (n: the first tile's first channel).  With
-// 8-byte stores a lane 8192 x 8192 x 7168 + r took 436 us, so 412; experts of 2003 tokens
-// 999 and 971.  (Non-temporal 8-byte stores: 515.)
+// 8-byte stores a lane 8192 x 8192 x 7168 + r took 436 us, so 412; experts of 2003 tokens,
+// when their rows were bf16, 999 and 971.  (Non-temporal 8-byte stores: 515.)
 __device__ __forceinline__ void trade(uint32_t& a, uint32_t& b) {
     const auto p = __builtin_amdgcn_permlane16_swap(a, b, false, false);
     a = p[0], b = p[1];

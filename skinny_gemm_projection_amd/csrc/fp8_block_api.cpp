@@ -98,7 +98,7 @@ bool step_layout(int32_t T, int32_t topk, int32_t E, int32_t H, int32_t F, StepL
     L->u = take(L->gated ? 0 : P * F * 8);
     L->p = take(P * F);
     L->sp = take(P * ((F + 127) / 128) * 4);
-    L->y = take(P * H * 2);
+    L->y = take(P * H * 4);
     L->total = at;
     return true;
 }
@@ -194,8 +194,8 @@ sg_status skinny_moe_combine(int32_t T, int32_t topk, int32_t K, const void* row
         !aligned(weights, 4))
         return SG_ERR_ALIGN;
     (void)hipGetLastError();
-    return done(sg::launch_moe_combine(rows, T, topk, pitch_of(K, f32), f32 != 0, positions, weights,
-                                       r, out, static_cast<hipStream_t>(stream)),
+    return done(sg::launch_moe_combine(rows, T, topk, pitch_of(K, f32), f32 != 0, f32 != 0, positions,
+                                       weights, r, out, static_cast<hipStream_t>(stream)),
                 SG_KERNEL_MOE_ROWS, 1, "moe_combine", T, topk, K);
 }
 
@@ -275,7 +275,7 @@ sg_status skinny_moe_fp8_step(const sg_moe_fp8_step* a, void* workspace, size_t 
     float* u = reinterpret_cast<float*>(base + L.u);
     uint8_t* p = reinterpret_cast<uint8_t*>(base + L.p);
     float* sp = reinterpret_cast<float*>(base + L.sp);
-    sg_bf16* y = reinterpret_cast<sg_bf16*>(base + L.y);
+    float* y = reinterpret_cast<float*>(base + L.y);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     sg_status st;
     if ((st = sort(T, topk, E, a->topk_ids, offsets, sorted, positions, base + L.sort, hs)) != SG_OK)
@@ -286,14 +286,14 @@ sg_status skinny_moe_fp8_step(const sg_moe_fp8_step* a, void* workspace, size_t 
     if (L.gated) up.N = F, up.y_f32 = nullptr, up.codes = p, up.scales = sp;
     if ((st = product(L.up, up, nullptr, hs)) != SG_OK) return st;
     if (!L.gated && (st = quant(P, F, u, true, true, p, sp, hs)) != SG_OK) return st;
-    // The rows of y are bf16, one rounding of 2^-8 each before the weighted sum in fp32, as
-    // large as the output's own: product and sum of 2003 tokens, 48 experts, take 370 us, with
-    // fp32 rows 446 and twice the workspace.
-    sg::Fp8Product down{p, sp, a->W_down, a->down_scales, P, H, F, P, nullptr, y, nullptr};
+    // The rows of y stay fp32 up to the weighted sum: rounded to bf16 they put as much error
+    // into out as its own rounding does, and all of out where experts cancel.  (Product
+    // and sum of 2003 tokens, 48 experts: 446 us, with bf16 rows 370.)
+    sg::Fp8Product down{p, sp, a->W_down, a->down_scales, P, H, F, P, y, nullptr, nullptr};
     down.offsets = offsets, down.E = E;
     if ((st = product(L.down, down, nullptr, hs)) != SG_OK) return st;
     (void)hipGetLastError();
-    return done(sg::launch_moe_combine(y, T, topk, (int64_t)H * 2, false, positions, a->topk_weights,
+    return done(sg::launch_moe_combine(y, T, topk, (int64_t)H * 4, true, false, positions, a->topk_weights,
                                        a->r, a->out, hs),
                 SG_KERNEL_MOE_ROWS, 1, "moe_combine", T, topk, H);
 }

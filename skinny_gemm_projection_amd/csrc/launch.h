@@ -222,7 +222,8 @@ hipError_t launch_moe_sort(const int32_t* ids, int P, int E, int32_t* offsets, i
                            int32_t* positions, void* ws, hipStream_t stream);
 hipError_t launch_moe_gather(const void* x, int T, int topk, int64_t pitch, const int32_t* positions,
                              void* rows, hipStream_t stream);
-hipError_t launch_moe_combine(const void* rows, int T, int topk, int64_t pitch, bool f32,
+// (out_f32: whether r and out are fp32 too; bf16 rows have bf16 ones)
+hipError_t launch_moe_combine(const void* rows, int T, int topk, int64_t pitch, bool f32, bool out_f32,
                               const int32_t* positions, const float* w, const void* r, void* out,
                               hipStream_t stream);
 hipError_t launch_moe_combine_grad(const void* d_out, const void* rows, int T, int topk,

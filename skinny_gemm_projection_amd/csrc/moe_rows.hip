@@ -320,19 +320,30 @@ struct Piece {  // 16 bytes of a row
 constexpr int kAtOnce = 8;  // rows of a token requested before the first is added
 
 // Sums in fp32, j ascending, each step one fused multiply-add (without weights an
-// addition); the residual is added last and the result rounded once.
-template <bool F32>
+// addition); the residual is added last and the result rounded once.  r and out have the
+// rows' type, or with NARROW bf16 beside rows of fp32.
+template <bool F32, bool NARROW>
 __global__ __launch_bounds__(kBlock) void moe_combine_kernel(
     const char* __restrict__ rows, int64_t pitch, int T, int topk,
     const int32_t* __restrict__ positions, const float* __restrict__ w, const char* r,
     char* out) {  // out may be r
+    static_assert(F32 || !NARROW, "bf16 rows have bf16 outputs");
     typedef Piece<F32> P;
+    constexpr int kShrink = NARROW ? 2 : 1;
     const int64_t t = token_of();
     const int64_t at = (int64_t)blockIdx.x * kSpan + threadIdx.x * 16;
     const int limit = T * topk;
     if (t >= T || at >= pitch) return;
     // requested with the rows, not behind their sum
-    const uint4 res = load16(make_rsrc(r + (r ? t : 0) * pitch, r ? (uint32_t)pitch : 0u), (uint32_t)at);
+    const int64_t opitch = pitch / kShrink, oat = at / kShrink;
+    const rsrc_t rr = make_rsrc(r + (r ? t : 0) * opitch, r ? (uint32_t)opitch : 0u);
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if constexpr (NARROW) {
+        const auto half = __builtin_amdgcn_raw_buffer_load_b64(rr, (uint32_t)oat, 0, 0);
+        res = make_uint4(half[0] << 16, half[0] & 0xffff0000u, half[1] << 16, half[1] & 0xffff0000u);
+    } else {
+        res = load16(rr, (uint32_t)oat);
+    }
     float acc[P::N] = {};
     for (int j0 = 0; j0 < topk; j0 += kAtOnce) {
         uint4 v[kAtOnce];
@@ -361,7 +372,11 @@ __global__ __launch_bounds__(kBlock) void moe_combine_kernel(
 #pragma unroll
         for (int k = 0; k < P::N; ++k) acc[k] = y[k] + acc[k];
     }
-    *reinterpret_cast<uint4*>(out + t * pitch + at) = P::pack(acc);
+    if constexpr (NARROW)
+        *reinterpret_cast<uint2*>(out + t * opitch + oat) =
+            make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
+    else
+        *reinterpret_cast<uint4*>(out + t * opitch + oat) = P::pack(acc);
 }
 
 // One workgroup a token.  The dot products of up to kAtOnce rows are held while the
@@ -501,10 +516,12 @@ hipError_t launch_moe_gather(const void* x, int T, int topk, int64_t pitch, cons
     return hipGetLastError();
 }
 
-hipError_t launch_moe_combine(const void* rows, int T, int topk, int64_t pitch, bool f32,
+hipError_t launch_moe_combine(const void* rows, int T, int topk, int64_t pitch, bool f32, bool out_f32,
                               const int32_t* positions, const float* w, const void* r, void* out,
                               hipStream_t stream) {
-    const auto kernel = f32 ? moe_combine_kernel<true> : moe_combine_kernel<false>;
+    const auto kernel = !f32      ? moe_combine_kernel<false, false>
+                        : out_f32 ? moe_combine_kernel<true, false>
+                                  : moe_combine_kernel<true, true>;
     hipLaunchKernelGGL(kernel, token_grid(T, pitch), dim3(kBlock), 0, stream,
                        static_cast<const char*>(rows), pitch, T, topk, positions, w,
                        static_cast<const char*>(r), static_cast<char*>(out));
